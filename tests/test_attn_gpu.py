@@ -1,0 +1,249 @@
+"""vqv_paged_attn against the oracle in 64 bits."""
+
+import pytest
+import torch
+
+from oracle import round_ref as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def vqv():
+    import w4_gemm_vqv_amd as v
+    v.lib()
+    return v
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Case:
+    """Inputs on the GPU. Every slot that no token stands in holds NaN, in K and V."""
+
+    def __init__(self, rows, kv, heads, hk, dim, ps, dtype="bf16", layout="slot", seed=0, layers=1,
+                 layer=0, max_rows=None, max_kv=None):
+        gen = torch.Generator().manual_seed(seed)
+        self.rows, self.kv, self.ps, self.hk, self.dim = rows, kv, ps, hk, dim
+        self.heads, self.t, self.layer = heads, DT[dtype], layer
+        self.start = [0]
+        for r in rows:
+            self.start.append(self.start[-1] + r)
+        self.n = self.start[-1]
+        held = [-(-x // ps) for x in kv]
+        self.pages = sum(held) + 3
+        perm = torch.randperm(self.pages, generator=gen).tolist()
+        self.table = [[-1] * (max(held) + 1) for _ in rows]
+        for b, x in enumerate(held):
+            for j in range(x):
+                self.table[b][j] = perm.pop()
+        shape = (layers, self.pages, ps, hk, dim)
+        k = torch.full(shape, float("nan"))
+        v = k.clone()
+        for b, x in enumerate(kv):
+            for t in range(x):
+                p = self.table[b][t // ps]
+                k[layer, p, t % ps] = torch.randn(hk, dim, generator=gen)
+                v[layer, p, t % ps] = torch.randn(hk, dim, generator=gen)
+        self.q = (1.5 * torch.randn(self.n, heads, dim, generator=gen)).to(self.t)
+        self.k, self.v = k.to(self.t), v.to(self.t)
+        self.layout = layout
+        self.max_rows = max(rows) if max_rows is None else max_rows
+        self.max_kv = max(kv) if max_kv is None else max_kv
+        self.scale = dim ** -0.5
+
+    def device(self, x):
+        if self.layout == "head":
+            return x.transpose(2, 3).contiguous().cuda().transpose(2, 3)
+        if self.layout == "gap":
+            wide = torch.full((*x.shape[:2], x.shape[2] + 1, x.shape[3], x.shape[4] + 8),
+                              float("nan"), dtype=x.dtype)
+            wide[:, :, :x.shape[2], :, :x.shape[4]] = x
+            return wide.cuda()[:, :, :x.shape[2], :, :x.shape[4]]
+        return x.cuda()
+
+    def run(self, vqv, window=0, sinks=0, stream=None, scale=None):
+        self.cache = vqv.PagedCache(self.device(self.k), self.device(self.v))
+        self.seqs = vqv.Sequences(i32(self.start), i32(self.kv), i32(self.table), n_rows=self.n,
+                                  max_rows=self.max_rows, max_kv=self.max_kv)
+        out = torch.full(self.q.shape, 9.0, dtype=self.t, device="cuda")
+        self.qd = self.q.cuda()
+        vqv.vqv_paged_attn(self.qd, self.cache, self.seqs, scale=scale or self.scale, window=window,
+                           sinks=sinks, layer=self.layer, out=out, stream=stream)
+        torch.cuda.synchronize()
+        return out.cpu()
+
+    def want(self, window=0, sinks=0, scale=None):
+        return ref.attn_ref(self.q, self.k[self.layer], self.v[self.layer], self.start, self.kv,
+                            self.table, scale or self.scale, window, sinks)
+
+    def close(self, got, want):
+        """Half a step of the output; half a step of each weight; a score's error moves its weight
+        by as much, relatively: `dim` products and sums in fp32 of sizes up to `size`, then one
+        scaling and one subtraction (2 roundings of values up to 2 * size) and the exponential
+        (2^-22), for the weight and for the sum of weights; sums over tokens in fp32. fp16 weights
+        below 2^-14 are off by up to 2^-14 (the smallest normal) each."""
+        out, mean, size = want
+        half, n = torch.finfo(self.t).eps / 2, max(self.kv)
+        score = size * (self.dim + 8) * 2.0 ** -24 + 2.0 ** -22
+        inner = (half + 2 * score + (n + 8) * 2.0 ** -24) * mean
+        if self.t == torch.float16:
+            inner = inner + n * 2.0 ** -14 * half * 8
+        allow = half * (out.abs() + inner) + inner + 2.0 ** -25
+        err = (got.double() - out).abs()
+        assert (err <= allow).all(), f"error over allowance {(err / allow).nan_to_num(1e9).max():.3g}"
+
+
+CASES = [
+    dict(rows=[1], kv=[1], heads=1, hk=1, dim=64, ps=1),
+    dict(rows=[8], kv=[300], heads=8, hk=2, dim=128, ps=16),
+    dict(rows=[1] * 5, kv=[1, 16, 129, 700, 64], heads=8, hk=2, dim=128, ps=16),
+    dict(rows=[3, 0, 1], kv=[40, 9, 33], heads=6, hk=2, dim=64, ps=20, dtype="fp16", layout="head"),
+    dict(rows=[16, 5], kv=[400, 37], heads=8, hk=2, dim=256, ps=32, dtype="fp16"),
+    dict(rows=[16, 16], kv=[16, 200], heads=12, hk=3, dim=96, ps=24, layout="gap"),
+    dict(rows=[70, 33], kv=[70, 401], heads=10, hk=2, dim=80, ps=8, layout="head"),
+    dict(rows=[130], kv=[333], heads=4, hk=4, dim=192, ps=64, dtype="fp16", layout="head"),
+    dict(rows=[65], kv=[257], heads=21, hk=3, dim=128, ps=128),
+    dict(rows=[100], kv=[164], heads=8, hk=1, dim=64, ps=1),
+    dict(rows=[40, 90], kv=[45, 91], heads=6, hk=2, dim=256, ps=16),
+    dict(rows=[9], kv=[77], heads=16, hk=2, dim=192, ps=20, layers=3, layer=1),
+    dict(rows=[12], kv=[90], heads=2, hk=1, dim=80, ps=16, dtype="fp16"),
+    dict(rows=[1, 1], kv=[2100, 5], heads=40, hk=1, dim=128, ps=64, layout="head"),
+    dict(rows=[2], kv=[1500], heads=2, hk=1, dim=96, ps=16),
+]
+WINDOWS = [(0, 0), (1, 0), (1, 3), (37, 0), (64, 4), (100, 150), (5000, 2)]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{c['rows']}kv{c['kv']}h{c['heads']}/{c['hk']}d{c['dim']}p{c['ps']}")
+def test_matches_oracle(vqv, case):
+    c = Case(**case)
+    c.close(c.run(vqv), c.want())
+
+
+@pytest.mark.parametrize("window,sinks", WINDOWS[1:])
+@pytest.mark.parametrize("index", [1, 2, 5, 6, 8, 10])
+def test_windows(vqv, index, window, sinks):
+    c = Case(**CASES[index])
+    c.close(c.run(vqv, window, sinks), c.want(window, sinks))
+
+
+def test_large_scores(vqv):
+    """Scores far apart: one weight takes nearly all, and moves from block to block."""
+    c = Case(rows=[8, 1], kv=[600, 900], heads=4, hk=2, dim=64, ps=16, seed=5)
+    c.q *= 12
+    c.close(c.run(vqv, scale=1.0), c.want(scale=1.0))
+
+
+def test_bad_pages_are_hidden(vqv):
+    """Pages that the table does not hold, or that are none: their tokens are
+    hidden; a row with nothing left gives zeros."""
+    for rows, heads in (([4, 6], 4), ([70, 40], 4)):
+        c = Case(rows=rows, kv=[160, 90], heads=heads, hk=2, dim=64, ps=16)
+        c.table[0][1], c.table[0][4], c.table[1][0] = -1, c.pages, 1 << 30
+        c.close(c.run(vqv), c.want())
+        for j in range(len(c.table[1])):
+            c.table[1][j] = -1
+        got = c.run(vqv)
+        c.close(got, c.want())
+        assert (got[rows[0]:] == 0).all()
+
+
+def test_past_the_table_and_lengths(vqv):
+    """kv_len past the table's width, shorter than the rows, zero."""
+    c = Case(rows=[3, 5, 2], kv=[64, 40, 20], heads=2, hk=1, dim=64, ps=16)
+    c.kv = [100, 3, 0]
+    c.max_kv = 100
+    got = c.run(vqv)
+    c.close(got, c.want())
+    assert (got[3:5] == 0).all() and (got[8:] == 0).all()
+
+
+def test_longer_than_planned(vqv):
+    """A max_kv below the real lengths costs speed, not results."""
+    for rows in ([2, 1], [80, 3]):
+        c = Case(rows=rows, kv=[900, 500], heads=4, hk=2, dim=128, ps=16, max_kv=150)
+        c.close(c.run(vqv), c.want())
+
+
+def test_rows_without_a_sequence(vqv):
+    """Rows past max_rows and past the last sequence are not written."""
+    c = Case(rows=[6], kv=[50], heads=2, hk=1, dim=64, ps=16, max_rows=4)
+    got, want = c.run(vqv), c.want()
+    assert (got[4:] == 9.0).all()
+    c.close(got[:4], tuple(x[:4] for x in want))
+
+
+def test_hidden_infinities_and_nan(vqv):
+    """Tokens that a row does not see may hold anything: future tokens of the
+    chunk, tokens before the window."""
+    for rows, dtype, dim in (([12], "bf16", 64), ([12], "fp16", 256), ([150], "bf16", 128)):
+        c = Case(rows=rows, kv=[200], heads=4, hk=1, dim=dim, ps=16, dtype=dtype)
+        n = rows[0]
+        clean = c.run(vqv, 40, 2)
+        for t, x in ((199, float("nan")), (200 - n // 2, float("inf")), (20, float("nan")),
+                     (21, float("-inf"))):
+            p = c.table[0][t // 16]
+            c.k[0, p, t % 16], c.v[0, p, t % 16] = x, x
+        got = c.run(vqv, 40, 2)
+        before = n // 2  # rows before the first bad token of the chunk that do not see 20, 21
+        rows_ok = [r for r in range(before) if 200 - n + r - 40 >= 21]
+        assert rows_ok and torch.equal(got[rows_ok], clean[rows_ok])
+        assert got[-1].isnan().all()
+
+
+def test_seen_nan(vqv):
+    """A NaN that is seen comes out."""
+    c = Case(rows=[2], kv=[40], heads=2, hk=1, dim=64, ps=16)
+    c.k[0, c.table[0][0], 3, 0, 5] = float("nan")
+    assert c.run(vqv).isnan().all()
+
+
+def test_deterministic_on_streams_and_graphs(vqv):
+    c = Case(rows=[8, 2], kv=[700, 90], heads=8, hk=2, dim=128, ps=16)
+    want = c.run(vqv)
+    assert torch.equal(c.run(vqv, stream=torch.cuda.Stream()), want)
+    out = torch.empty(c.q.shape, dtype=c.t, device="cuda")
+    need = vqv.vqv_paged_attn_workspace_bytes(c.cache, c.seqs, c.heads)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        vqv.vqv_paged_attn(c.qd, c.cache, c.seqs, scale=c.scale, out=out, workspace=ws)
+    for _ in range(4):
+        out.zero_()
+        ws.fill_(255)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want)
+
+
+def test_far_offsets(vqv):
+    """Pages whose place passes 2^32 values."""
+    ps, hk, dim, pages = 64, 8, 256, 36000        # 36000 pages of 131072 values: 4.7e9
+    k = torch.empty((1, pages, ps, hk, dim), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    ids = [pages - 1, 5, pages - 2]
+    gen = torch.Generator().manual_seed(1)
+    small = [torch.randn(3, ps, hk, dim, generator=gen).to(torch.bfloat16) for _ in range(2)]
+    for x, s in zip((k, v), small):
+        x[0, ids] = s.cuda()
+    q = torch.randn(2, hk, dim, generator=gen).to(torch.bfloat16)
+    seqs = vqv.Sequences(i32([0, 2]), i32([150]), i32([ids]), n_rows=2, max_rows=2, max_kv=150)
+    got = vqv.vqv_paged_attn(q.cuda(), vqv.PagedCache(k, v), seqs, scale=0.06).cpu()
+    c = Case(rows=[2], kv=[150], heads=hk, hk=hk, dim=dim, ps=ps)
+    c.close(got, ref.attn_ref(q, *small, [0, 2], [150], [[0, 1, 2]], 0.06))
+
+
+def test_refuses_wrong_tensors(vqv):
+    c = Case(rows=[2], kv=[10], heads=2, hk=1, dim=64, ps=16)
+    c.run(vqv)
+    for q in (c.qd[:1], c.qd.half(), c.qd[:, :, ::2], c.qd[:, 0], c.q):
+        with pytest.raises(ValueError):
+            vqv.vqv_paged_attn(q, c.cache, c.seqs, scale=1.0)
+    with pytest.raises(ValueError):
+        vqv.vqv_paged_attn(c.qd, c.cache, c.seqs, scale=1.0, out=torch.empty(2, 2, 64, device="cuda"))
+    with pytest.raises(vqv.VqvError):
+        vqv.vqv_paged_attn(c.qd, c.cache, c.seqs, scale=0.0)

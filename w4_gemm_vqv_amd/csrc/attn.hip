@@ -1,0 +1,584 @@
+// Attention of new rows over a paged cache (vqv_paged_attn).
+//
+// The query rows of a sequence that share a key head, (row, head) pairs with
+// the head fastest, are cut into tiles of 32 per wave; a work-group of MW x KW
+// waves walks over the visible tokens in blocks of KW * KT, staged in LDS, so
+// that every wave reads each key and value once from there whatever the page
+// size and layout. Wave (mw, kw) takes query tile mw and the kw-th KT tokens
+// of each block. With few query rows (plain decoding, verify blocks) the
+// waves split the tokens (KW > 1), and long sequences are also split over
+// work-groups, whose partial sums a second kernel joins.
+//
+// A wave forms S^T = K Q^T with 32x32x16 matrix instructions: lane l holds 16
+// scores of each 32 tokens for query row l % 32, so maxima and sums stay in
+// the lane but for one exchange with lane l ^ 32. Accumulator rows of lane
+// half h are the tokens 8i + 4h + 0..3; read as the B operand of O^T = V^T
+// P^T these are the k slots 8h + 0..7 of a 16-token step if the step's tokens
+// are taken in the order 4h..4h+3, 8+4h..8+4h+3. V^T is read in that order
+// (the transposing LDS read gives a lane four tokens of one column), so P
+// needs no exchange at all.
+//
+// Softmax runs with base-2 exponentials and a running maximum; scores, maxima,
+// sums and outputs are fp32. P is rounded to the cache's type, the matrix
+// instruction's input: an error of at most half a step of each weight, which
+// the sum over tokens averages.
+
+#include "round_common.h"
+#include "round_internal.h"
+
+namespace vqv {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) short s16x8;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(16))) float f32x16;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+
+struct AttnArgs {
+  const void* q;
+  void* out;
+  const void* k;  // of the layer
+  const void* v;
+  vqv_seqs seqs;
+  int page_size, pages, kv_heads, group;  // group: query heads per key head
+  unsigned page_units, slot_units, head_units;  // strides in 16-byte units
+  float scale_log2;
+  int window, sinks;
+  int tiles, split_blocks, splits;
+  float* part;  // [n_rows * heads][splits][dim] sums, then [..][splits][2] (max, sum)
+  float* part_ml;
+};
+
+template <typename T>
+__device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c);
+template <>
+__device__ __forceinline__ f32x16 mfma<__bf16>(s16x8 a, s16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+template <>
+__device__ __forceinline__ f32x16 mfma<_Float16>(s16x8 a, s16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+template <typename T>
+__device__ __forceinline__ unsigned pack2(float a, float b) {
+  typedef __attribute__((ext_vector_type(2))) T t2;
+  const t2 r = {(T)a, (T)b};
+  return __builtin_bit_cast(unsigned, r);
+}
+
+template <typename T>
+struct Bits;  // of a type: its exponent, and 1
+template <>
+struct Bits<__bf16> {
+  static constexpr unsigned exponent = 0x7F80u, one = 0x3F80u;
+};
+template <>
+struct Bits<_Float16> {
+  static constexpr unsigned exponent = 0x7C00u, one = 0x3C00u;
+};
+
+// Not 0 where one of two packed values is an infinity or NaN: an exponent of
+// ones carries into the sign's place.
+template <typename T>
+__device__ __forceinline__ unsigned not_finite(unsigned w) {
+  constexpr unsigned e = Bits<T>::exponent, low = e & (0u - e);
+  return ((w & (e | e << 16)) + (low | low << 16)) & 0x80008000u;
+}
+
+// Takes the infinities and NaN out of the values `va` (tokens in a lane's
+// order, `seen` their bits for the lane's query row) and adds what they come
+// to: where a row sees one, the infinity, or both (NaN). Which rows see one is
+// a product of zeros and ones.
+template <typename T>
+__device__ void add_not_finite(s16x8& va, unsigned seen, f32x16& o) {
+  constexpr unsigned e = Bits<T>::exponent;
+  s16x8 up = {}, down = {}, see = {};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const unsigned w = (unsigned short)va[i];
+    const bool out = (w & e) == e, nan = out && (w & 0x7FFFu) != e;
+    up[i] = out && (nan || !(w & 0x8000u)) ? Bits<T>::one : 0;
+    down[i] = out && (nan || (w & 0x8000u)) ? Bits<T>::one : 0;
+    see[i] = seen >> i & 1u ? Bits<T>::one : 0;
+    va[i] = out ? 0 : va[i];
+  }
+  const f32x16 a = mfma<T>(up, see, f32x16{}), b = mfma<T>(down, see, f32x16{});
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (a[i] != 0.0f) o[i] += __builtin_inff();
+    if (b[i] != 0.0f) o[i] -= __builtin_inff();
+  }
+}
+
+// Which 16-byte piece of a staged row of DC pieces holds piece c. Without the
+// exchange the rows that one LDS access touches would begin in the same
+// banks. Keys are read 8 rows at a time, one piece each; values 4 rows at a
+// time, 4 pieces each.
+template <int DC>
+__device__ __forceinline__ int k_piece(int row, int c) {
+  if (DC % 8 == 0) return c ^ (row & 7);
+  if (DC == 12) return c ^ (row >> 2 & 1);
+  return c;
+}
+template <int DC>
+__device__ __forceinline__ int v_piece(int row, int c) {
+  if (DC % 16 == 0) return c ^ ((row & 3) << 2);
+  if (DC % 8 == 0) return c ^ ((row >> 1 & 1) << 2);
+  return c;
+}
+
+// The tokens that the rows of a tile see, as blocks of BT tokens: `sink`
+// blocks from token 0 on, then those from block `first` on; `all` in total.
+struct Blocks {
+  int sink, first, all;
+};
+
+template <int BT>
+__device__ __forceinline__ Blocks visible_blocks(int p0, int p1, int kv_len, int window,
+                                                 int sinks) {
+  const int hi = min(p1 + 1, kv_len);
+  if (hi <= 0) return Blocks{0, 0, 0};
+  const int lo = window > 0 ? max(p0 - window + 1, 0) : 0;
+  const int sink_end = min(sinks, lo);
+  Blocks r;
+  r.sink = window > 0 && sink_end > 0 ? (sink_end + BT - 1) / BT : 0;
+  const int last = (hi + BT - 1) / BT;
+  r.sink = min(r.sink, last);
+  r.first = max(lo / BT, r.sink);
+  r.all = r.sink + max(last - r.first, 0);
+  return r;
+}
+
+// Blocks of a split: the plan's, or more where a sequence is longer than the
+// plan was made for.
+__device__ __forceinline__ int blocks_of_split(const AttnArgs& a, int all) {
+  return max(a.split_blocks, (all + a.splits - 1) / a.splits);
+}
+
+template <typename T, int D, int MW, int KW, int KT>
+__global__ __launch_bounds__(MW * KW * 64) void paged_attn(const AttnArgs a) {
+  constexpr int NW = MW * KW, BT = KW * KT, DC = D / 8, DS = D / 16, DB = (D + 31) / 32;
+  constexpr int NT = NW * 64;
+  constexpr int PIECES = BT * DC;                    // of the keys of a block
+  constexpr int LOADS = (PIECES + NT - 1) / NT;      // per thread
+  constexpr int SUB = KT / 32;
+  constexpr int STAGE = BT * D;                      // values of K (or V) of a block
+  // One more row: the last column block of V reads past its row where D is
+  // not a multiple of 32 (the results are not used).
+  constexpr int VSTAGE = STAGE + 32;
+  __shared__ __align__(16) uint16_t lds[2 * (STAGE + VSTAGE)];
+
+  const int h = blockIdx.x % a.kv_heads;
+  const int b = blockIdx.x / a.kv_heads % a.seqs.n_seqs;
+  const int rest = blockIdx.x / a.kv_heads / a.seqs.n_seqs;
+  const int tile = a.tiles - 1 - rest % a.tiles;  // the longest first
+  const int split = rest / a.tiles;
+
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int mw = wave % MW, kw = wave / MW;
+  const int half = lane >> 5, ql = lane & 31;
+
+  const int row0 = max(a.seqs.row_start[b], 0);
+  const int n = min(min(a.seqs.row_start[b + 1], a.seqs.n_rows) - row0, a.seqs.max_rows);
+  const int g = a.group;
+  const int m0 = tile * MW * 32;
+  if (m0 >= n * g) return;
+  const int kv_len = a.seqs.kv_len[b];
+  const int pos0 = kv_len - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
+  const int p0 = pos0 + m0 / g, p1 = pos0 + (min(m0 + MW * 32, n * g) - 1) / g;
+  const Blocks blocks = visible_blocks<BT>(p0, p1, kv_len, a.window, a.sinks);
+  const int per_split = blocks_of_split(a, blocks.all);
+  const int parts = max((blocks.all + per_split - 1) / per_split, 1);
+  if (split >= parts) return;
+  const int j0 = split * per_split, j1 = min(j0 + per_split, blocks.all);
+
+  // This lane's query row, and its values as the B operand.
+  const int m = m0 + mw * 32 + ql;
+  const bool real = m < n * g;
+  const int qrow = real ? m / g : 0, qhead = h * g + (real ? m - qrow * g : 0);
+  const int pos = real ? pos0 + qrow : -1;
+  const int64_t qi = ((int64_t)(row0 + qrow) * (a.kv_heads * g) + qhead) * D;
+  s16x8 qf[DS];
+#pragma unroll
+  for (int s = 0; s < DS; ++s) {
+    qf[s] = s16x8{};
+    if (real)
+      qf[s] = *reinterpret_cast<const s16x8*>(static_cast<const uint16_t*>(a.q) + qi + 16 * s +
+                                              8 * half);
+  }
+
+  f32x16 o[DB];
+#pragma unroll
+  for (int d = 0; d < DB; ++d) o[d] = f32x16{};
+  float mx = -__builtin_inff(), sum = 0.0f;
+
+  u32x4 kr[LOADS], vr[LOADS];
+  const auto base_of = [&](int j) {
+    return (j < blocks.sink ? j : blocks.first + j - blocks.sink) * BT;
+  };
+  const auto load = [&](int j) {
+    const int t0 = base_of(j);
+#pragma unroll
+    for (int x = 0; x < LOADS; ++x) {
+      const int p = x * NT + threadIdx.x;
+      const int t = t0 + p / DC, c = p % DC;
+      kr[x] = u32x4{};
+      vr[x] = u32x4{};
+      if (p < PIECES && t < kv_len) {
+        const int page = page_of(a.seqs, b, t, a.page_size, a.pages);
+        if (page >= 0) {
+          const uint64_t u = (uint64_t)page * a.page_units +
+                             (uint64_t)(t % a.page_size) * a.slot_units +
+                             (uint64_t)h * a.head_units + c;
+          kr[x] = static_cast<const u32x4*>(a.k)[u];
+          vr[x] = static_cast<const u32x4*>(a.v)[u];
+        }
+      }
+    }
+  };
+  const auto store = [&](int buf) {
+    uint16_t* ks = lds + buf * (STAGE + VSTAGE);
+    uint16_t* vs = ks + STAGE;
+#pragma unroll
+    for (int x = 0; x < LOADS; ++x) {
+      const int p = x * NT + threadIdx.x;
+      const int t = p / DC, c = p % DC;
+      if (p < PIECES) {
+        *reinterpret_cast<u32x4*>(ks + t * D + k_piece<DC>(t, c) * 8) = kr[x];
+        *reinterpret_cast<u32x4*>(vs + t * D + v_piece<DC>(t, c) * 8) = vr[x];
+      }
+    }
+  };
+
+  if (j0 < j1) {
+    load(j0);
+    store(0);
+  }
+  for (int j = j0; j < j1; ++j) {
+    const int buf = (j - j0) & 1;
+    if (j + 1 < j1) load(j + 1);
+    __syncthreads();
+    const uint16_t* ks = lds + buf * (STAGE + VSTAGE) + kw * KT * D;
+    const uint16_t* vs = lds + buf * (STAGE + VSTAGE) + STAGE + kw * KT * D;
+    const int t0 = base_of(j) + kw * KT;
+
+    f32x16 s[SUB];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      s[u] = f32x16{};
+#pragma unroll
+      for (int x = 0; x < DS; ++x) {
+        const int row = 32 * u + ql;
+        const s16x8 kf = *reinterpret_cast<const s16x8*>(
+            ks + row * D + k_piece<DC>(row, 2 * x + half) * 8);
+        s[u] = mfma<T>(kf, qf[x], s[u]);
+      }
+    }
+    // Hidden tokens, and those without a page. Where every row sees every token
+    // there is nothing to mask.
+    bool full = t0 + KT - 1 <= p0 && (a.window == 0 || t0 > p1 - a.window);
+    unsigned paged[SUB], seen = 0;
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      const int tk = t0 + 32 * u + ql;
+      paged[u] =
+          (unsigned)__ballot(tk < kv_len && page_of(a.seqs, b, tk, a.page_size, a.pages) >= 0);
+      full = full && paged[u] == ~0u;
+    }
+    if (!full) {
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int k = 8 * (i / 4) + 4 * half + (i & 3), t = t0 + 32 * u + k;
+          bool see = t <= pos && (paged[u] >> k & 1u);
+          if (a.window > 0) see = see && (t > pos - a.window || t < a.sinks);
+          s[u][i] = see ? s[u][i] : -__builtin_inff();
+          seen |= (see ? 1u : 0u) << (16 * u + i);
+        }
+    }
+    float top = mx;
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float shift = top == -__builtin_inff() ? 0.0f : top * a.scale_log2;
+    const float back = mx == -__builtin_inff() ? 0.0f
+                                               : __builtin_amdgcn_exp2f(mx * a.scale_log2 - shift);
+    mx = top;
+    sum *= back;
+#pragma unroll
+    for (int u = 0; u < SUB; ++u)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], a.scale_log2, -shift));
+        sum += s[u][i];
+      }
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[d][i] *= back;
+
+    // A hidden token's weight is 0, which an infinity or NaN of its values
+    // would turn into NaN: where some rows do not see all tokens, such values
+    // are looked for and left out of the product.
+    bool bad = false;
+    if (!full) {
+      unsigned found = 0;
+      for (int x = lane; x < KT * DC; x += 64) {
+        const u32x4 w = *reinterpret_cast<const u32x4*>(vs + x * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) found |= not_finite<T>(w[e]);
+      }
+      bad = __ballot(found != 0) != 0;
+    }
+#pragma unroll
+    for (int u = 0; u < 2 * SUB; ++u) {
+      u32x4 pw;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pw[i] = pack2<T>(s[u / 2][8 * (u & 1) + 2 * i], s[u / 2][8 * (u & 1) + 2 * i + 1]);
+      const s16x8 pf = __builtin_bit_cast(s16x8, pw);
+#pragma unroll
+      for (int d = 0; d < DB; ++d) {
+        // Lane l of 16 reads 4 columns of token l / 4; it gets 4 tokens of column l % 16.
+        s16x4 vf[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int row = 16 * u + 8 * y + 4 * half + (lane >> 2 & 3);
+          const int col = 32 * d + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+          const uint16_t* p = vs + row * D + v_piece<DC>(row, col >> 3) * 8 + (col & 7);
+          vf[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)p);
+        }
+        s16x8 va = __builtin_shufflevector(vf[0], vf[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        if (bad) add_not_finite<T>(va, seen >> (8 * u), o[d]);
+        o[d] = mfma<T>(va, pf, o[d]);
+      }
+    }
+    if (j + 1 < j1) store(1 - buf);
+  }
+  sum += __shfl_xor(sum, 32);
+
+  // Waves that split the tokens join their sums through LDS, half of them at
+  // a time.
+  if (KW > 1) {
+    float* x = reinterpret_cast<float*>(lds);
+    constexpr int PER = DB * 16 + 2;
+#pragma unroll
+    for (int w = KW / 2; w >= 1; w >>= 1) {
+      __syncthreads();
+      float* mine = x + (((kw % w) * MW + mw) * PER) * 64 + lane;
+      if (kw >= w && kw < 2 * w) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[(d * 16 + i) * 64] = o[d][i];
+        mine[DB * 16 * 64] = mx;
+        mine[(DB * 16 + 1) * 64] = sum;
+      }
+      __syncthreads();
+      if (kw < w) {
+        const float om = mine[DB * 16 * 64], os = mine[(DB * 16 + 1) * 64];
+        const float top = fmaxf(mx, om);
+        const float shift = top == -__builtin_inff() ? 0.0f : top * a.scale_log2;
+        const float fa = __builtin_amdgcn_exp2f(mx * a.scale_log2 - shift);
+        const float fb = __builtin_amdgcn_exp2f(om * a.scale_log2 - shift);
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][i] = o[d][i] * fa + mine[(d * 16 + i) * 64] * fb;
+        sum = sum * fa + os * fb;
+        mx = top;
+      }
+    }
+    if (kw > 0) return;
+  }
+
+  if (!real) return;
+  if (parts == 1) {
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + qi;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = 32 * d + 8 * i + 4 * half;
+        if (col < D) {
+          u32x2 w = {pack2<T>(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
+                     pack2<T>(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+          *reinterpret_cast<u32x2*>(out + col) = w;
+        }
+      }
+  } else {
+    const int64_t at = ((int64_t)(row0 + qrow) * (a.kv_heads * g) + qhead) * a.splits + split;
+    float* out = a.part + at * D;
+#pragma unroll
+    for (int d = 0; d < DB; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int col = 32 * d + 8 * i + 4 * half;
+        if (col < D)
+          *reinterpret_cast<f32x4*>(out + col) =
+              f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+      }
+    if (half == 0) {
+      a.part_ml[2 * at] = mx;
+      a.part_ml[2 * at + 1] = sum;
+    }
+  }
+}
+
+// Joins the partial sums of a (row, head): one wave, 4 columns per lane.
+template <typename T, int BT>
+__global__ __launch_bounds__(64) void paged_attn_join(const AttnArgs a, int rows_per_tile,
+                                                      int D) {
+  const int heads = a.kv_heads * a.group;
+  const int r = blockIdx.x / heads, head = blockIdx.x % heads;
+  const int b = seq_of_row(a.seqs.row_start, a.seqs.n_seqs, r);
+  if (b >= a.seqs.n_seqs) return;
+  const int row0 = max(a.seqs.row_start[b], 0);
+  if (r < row0) return;
+  const int n = min(min(a.seqs.row_start[b + 1], a.seqs.n_rows) - row0, a.seqs.max_rows);
+  if (r - row0 >= n) return;
+  const int g = a.group, kv_len = a.seqs.kv_len[b];
+  const int pos0 = kv_len - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
+  const int m0 = ((r - row0) * g + head % g) / rows_per_tile * rows_per_tile;
+  const int p0 = pos0 + m0 / g, p1 = pos0 + (min(m0 + rows_per_tile, n * g) - 1) / g;
+  const Blocks blocks = visible_blocks<BT>(p0, p1, kv_len, a.window, a.sinks);
+  const int per_split = blocks_of_split(a, blocks.all);
+  const int parts = (blocks.all + per_split - 1) / per_split;
+  if (parts <= 1) return;  // written by the first kernel
+  const int64_t at = (int64_t)blockIdx.x * a.splits;
+  float top = -__builtin_inff();
+  for (int s = 0; s < parts; ++s) top = fmaxf(top, a.part_ml[2 * (at + s)]);
+  const float shift = top == -__builtin_inff() ? 0.0f : top * a.scale_log2;
+  const int col = threadIdx.x * 4;
+  f32x4 o = {};
+  float sum = 0.0f;
+  for (int s = 0; s < parts; ++s) {
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (at + s)] * a.scale_log2 - shift);
+    sum += f * a.part_ml[2 * (at + s) + 1];
+    if (col < D) o += f * *reinterpret_cast<const f32x4*>(a.part + (at + s) * D + col);
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (col < D) {
+    const u32x2 w = {pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv)};
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (int64_t)blockIdx.x * D + col) = w;
+  }
+}
+
+template <typename T, int D, int MW, int KW, int KT>
+hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
+  const int64_t grid = (int64_t)a.kv_heads * a.seqs.n_seqs * a.tiles * a.splits;
+  hipLaunchKernelGGL((paged_attn<T, D, MW, KW, KT>), dim3((unsigned)grid), dim3(MW * KW * 64), 0,
+                     stream, a);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  hipLaunchKernelGGL((paged_attn_join<T, KW * KT>),
+                     dim3((unsigned)(a.seqs.n_rows * a.kv_heads * a.group)), dim3(64), 0, stream,
+                     a, MW * 32, D);
+  return hipGetLastError();
+}
+
+template <typename T, int D>
+hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  constexpr bool wide = D > 128;
+  if (p.mw == 4) return launch_shape<T, D, 4, 1, wide ? 32 : 64>(a, stream);
+  if (p.mw == 2) return launch_shape<T, D, 2, 2, 32>(a, stream);
+  return launch_shape<T, D, 1, wide ? 2 : 4, 32>(a, stream);
+}
+
+template <typename T>
+hipError_t launch_type(const AttnArgs& a, int dim, const AttnPlan& p, hipStream_t stream) {
+  switch (dim) {
+    case 64: return launch_dim<T, 64>(a, p, stream);
+    case 80: return launch_dim<T, 80>(a, p, stream);
+    case 96: return launch_dim<T, 96>(a, p, stream);
+    case 128: return launch_dim<T, 128>(a, p, stream);
+    case 192: return launch_dim<T, 192>(a, p, stream);
+    default: return launch_dim<T, 256>(a, p, stream);
+  }
+}
+
+int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+}  // namespace
+
+bool attn_dim_supported(int dim) {
+  return dim == 64 || dim == 80 || dim == 96 || dim == 128 || dim == 192 || dim == 256;
+}
+
+AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window, int sinks) {
+  const bool wide = c.dim > 128;
+  const int64_t m = (int64_t)(s.max_rows < s.n_rows ? s.max_rows : s.n_rows) * (heads / c.kv_heads);
+  AttnPlan p;
+  p.mw = m <= 32 ? 1 : m <= 64 ? 2 : 4;
+  p.kw = p.mw == 4 ? 1 : p.mw == 2 ? 2 : wide ? 2 : 4;
+  p.kt = p.mw == 4 && !wide ? 64 : 32;
+  p.tiles = ceil_div(m < 1 ? 1 : m, 32 * p.mw);
+  const int bt = p.kw * p.kt;
+  // The most blocks that a tile's rows see.
+  int64_t tokens = s.max_kv;
+  if (window > 0) {
+    const int64_t rows_of_tile = 32 * p.mw / (heads / c.kv_heads) + 2;
+    int64_t seen = (int64_t)window + rows_of_tile + 2 * bt;
+    seen += sinks < s.max_kv ? sinks + bt : s.max_kv;
+    tokens = seen < tokens ? seen : tokens;
+  }
+  const int blocks = ceil_div(tokens < 1 ? 1 : tokens, bt);
+  // Work-groups wanted: several rounds over the CUs where the tokens are the
+  // work (their lengths differ), one round of two per CU for full tiles.
+  const int64_t base = (int64_t)c.kv_heads * s.n_seqs * p.tiles;
+  const int64_t want = p.mw == 4 ? 512 : 2048;
+  const int least = p.mw == 4 ? 4 : 1;  // blocks of a split
+  int64_t splits = want / (base < 1 ? 1 : base);
+  if (splits < 1) splits = 1;
+  p.split_blocks = ceil_div(blocks, splits);
+  if (p.split_blocks < least) p.split_blocks = least;
+  p.splits = ceil_div(blocks, p.split_blocks);
+  return p;
+}
+
+size_t attn_partial_bytes(const vqv_cache& c, const vqv_seqs& s, int heads, const AttnPlan& p) {
+  if (p.splits <= 1) return 0;
+  return (size_t)s.n_rows * heads * p.splits * (c.dim + 2) * sizeof(float);
+}
+
+hipError_t launch_paged_attn(const void* q, const vqv_cache& c, int layer, const vqv_seqs& seqs,
+                             int heads, float scale, int window, int sinks, void* out,
+                             void* workspace, const AttnPlan& plan, hipStream_t stream) {
+  AttnArgs a{};
+  a.q = q;
+  a.out = out;
+  a.k = static_cast<const uint16_t*>(c.k) + layer * c.layer_stride;
+  a.v = static_cast<const uint16_t*>(c.v) + layer * c.layer_stride;
+  a.seqs = seqs;
+  a.page_size = c.page_size;
+  a.pages = c.pages;
+  a.kv_heads = c.kv_heads;
+  a.group = heads / c.kv_heads;
+  a.page_units = (unsigned)(c.page_stride >> 3);
+  a.slot_units = (unsigned)(c.slot_stride >> 3);
+  a.head_units = (unsigned)(c.head_stride >> 3);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.window = window;
+  a.sinks = window > 0 ? sinks : 0;
+  a.tiles = plan.tiles;
+  a.split_blocks = plan.split_blocks;
+  a.splits = plan.splits;
+  a.part = static_cast<float*>(workspace);
+  a.part_ml = a.part + (size_t)seqs.n_rows * heads * plan.splits * c.dim;
+  return c.dtype == VQV_BF16 ? launch_type<__bf16>(a, c.dim, plan, stream)
+                             : launch_type<_Float16>(a, c.dim, plan, stream);
+}
+
+}  // namespace vqv

@@ -1,0 +1,456 @@
+// Pages of a cache: copy, fork, trim, reserve, and the compaction of a
+// block's confirmed rows.
+//
+// The book (which table holds which page) is small: one work-group or one
+// wave per row does it. The moves of keys and values are spread over the
+// whole GPU in 16-byte pieces; they are bound by memory. Sums of references
+// are integer atomics, so their order does not matter, and free pages are
+// given out by rank (prefix sums), so the result does not depend on timing.
+
+#include <limits.h>
+
+#include "round_common.h"
+#include "round_internal.h"
+
+namespace vqv {
+namespace {
+
+constexpr int kBook = 1024;           // threads of the book's work-group
+constexpr int kPer = 16;              // pages per thread and step of its scan
+constexpr int kStep = kBook * kPer;
+
+struct Int4 {  // four references; rows of any 4-byte alignment
+  int v[4];
+};
+
+// Inclusive scan over the kBook threads of the work-group; total in *all.
+__device__ int scan_block(int x, int* waves, int* all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int s = x;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int o = __shfl_up(s, d);
+    if (lane >= d) s += o;
+  }
+  __syncthreads();  // `waves` may still be read from the last call
+  if (lane == 63) waves[wave] = s;
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kBook / 64; ++w) {
+    const int t = waves[w];
+    before += w < wave ? t : 0;
+    sum += t;
+  }
+  *all = sum;
+  return before + s;
+}
+
+// Bits of the free pages among p0 .. p0 + kPer - 1.
+__device__ unsigned free_bits(const int32_t* __restrict__ ref, int pages, int p0) {
+  unsigned m = 0;
+  if (p0 + kPer <= pages) {
+#pragma unroll
+    for (int q = 0; q < kPer / 4; ++q) {
+      Int4 r;
+      __builtin_memcpy(&r, ref + p0 + 4 * q, sizeof(r));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m |= (r.v[e] == 0 ? 1u : 0u) << (4 * q + e);
+    }
+  } else {
+    for (int e = 0; e < kPer && p0 + e < pages; ++e) m |= (ref[p0 + e] == 0 ? 1u : 0u) << e;
+  }
+  return m;
+}
+
+// How many pages are free, counted only until `enough`.
+__device__ int count_free(const int32_t* __restrict__ ref, int pages, int enough, int* waves) {
+  int found = 0;
+  for (int base = 0; base < pages && found < enough; base += kStep) {
+    int all;
+    scan_block(__popc(free_bits(ref, pages, base + threadIdx.x * kPer)), waves, &all);
+    found += all;
+  }
+  return found;
+}
+
+// Calls give(rank, page) for the `want` lowest free pages, and marks them
+// with one reference. off[] (n entries, ascending) is left to `give`.
+template <typename F>
+__device__ void give_free(int32_t* __restrict__ ref, int pages, int want, int* waves, F give) {
+  int found = 0;
+  for (int base = 0; base < pages && found < want; base += kStep) {
+    const int p0 = base + threadIdx.x * kPer;
+    unsigned m = free_bits(ref, pages, p0);
+    const int mine = __popc(m);
+    int all;
+    int rank = found + scan_block(mine, waves, &all) - mine;
+    while (m && rank < want) {
+      const int p = p0 + __ffs(m) - 1;
+      m &= m - 1;
+      ref[p] = 1;
+      give(rank, p);
+      ++rank;
+    }
+    found += all;
+  }
+}
+
+// The last of n entries with off[i] <= rank.
+__device__ int owner_of(const int32_t* off, int n, int rank) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= rank) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ int pages_for(int tokens, int page_size) {
+  return tokens <= 0 ? 0 : (tokens - 1) / page_size + 1;
+}
+
+__device__ __forceinline__ int clamp_int(int x, int lo, int hi) {
+  return x < lo ? lo : x > hi ? hi : x;
+}
+
+// One wave per row. A page leaves the table by an exchange, so a row that is
+// named twice gives each page back once.
+__global__ __launch_bounds__(64) void cache_trim(const vqv_pages pg,
+                                                 const int32_t* __restrict__ keep_len,
+                                                 const int32_t* __restrict__ rows) {
+  const int i = blockIdx.x;
+  const int row = rows ? rows[i] : i;
+  if ((unsigned)row >= (unsigned)pg.rows) return;
+  const int keep = max(keep_len[i], 0);
+  const int held = clamp_int(pg.held[row], 0, pg.width);
+  const int length = pg.length[row];
+  const int stay = pages_for(keep, pg.page_size);
+  int32_t* t = pg.table + (int64_t)row * pg.width;
+  for (int j = stay + (int)threadIdx.x; j < held; j += 64) {
+    const int p = atomicExch(&t[j], -1);
+    if ((unsigned)p < (unsigned)pg.pages) atomicSub(&pg.ref[p], 1);
+  }
+  if (threadIdx.x == 0) {
+    if (stay < held) pg.held[row] = stay;
+    if (keep < length) pg.length[row] = keep;
+  }
+}
+
+// One work-group. off[]: the rank of each row's first new page.
+__global__ __launch_bounds__(kBook) void cache_reserve(const vqv_pages pg,
+                                                       const int32_t* __restrict__ goal_len,
+                                                       int n, int32_t* __restrict__ ok,
+                                                       int32_t* __restrict__ off) {
+  __shared__ int waves[kBook / 64];
+  __shared__ int granted;
+  if (threadIdx.x == 0) granted = 0;
+  int total = 0;
+  for (int base = 0; base < n; base += kBook) {
+    const int i = base + threadIdx.x;
+    int need = 0;
+    if (i < n) {
+      const int goal = pages_for(goal_len[i], pg.page_size);
+      const int held = clamp_int(pg.held[i], 0, pg.width);
+      need = goal <= pg.width ? max(goal - held, 0) : 0;
+    }
+    int all;
+    const int end = scan_block(need, waves, &all);
+    if (i < n) off[i] = total + end - need;
+    total = min(total + all, INT_MAX / 2);
+  }
+  const int found = total ? count_free(pg.ref, pg.pages, total, waves) : 0;
+  for (int i = threadIdx.x; i < n; i += kBook) {
+    const int goal = pages_for(goal_len[i], pg.page_size);
+    const int held = clamp_int(pg.held[i], 0, pg.width);
+    const int need = goal <= pg.width ? max(goal - held, 0) : 0;
+    const bool good = goal <= pg.width && (need == 0 || off[i] + need <= found);
+    ok[i] = good;
+    if (good && need) atomicMax(&granted, off[i] + need);
+  }
+  __syncthreads();
+  const int want = granted;
+  give_free(pg.ref, pg.pages, want, waves, [&](int rank, int p) {
+    const int i = owner_of(off, n, rank);
+    const int held = clamp_int(pg.held[i], 0, pg.width);
+    pg.table[(int64_t)i * pg.width + held + rank - off[i]] = p;
+  });
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kBook)
+    if (ok[i]) {
+      const int goal = pages_for(goal_len[i], pg.page_size);
+      if (goal > pg.held[i]) pg.held[i] = goal;
+    }
+}
+
+// The book of a fork, one work-group: which pairs are good, their new pages,
+// the children's tables; from[i] and to[i] are the pages to copy, or -1.
+__global__ __launch_bounds__(kBook) void cache_fork_book(
+    const vqv_pages pg, const int32_t* __restrict__ parent, const int32_t* __restrict__ child,
+    int n, int32_t* __restrict__ ok, int32_t* __restrict__ named, int32_t* __restrict__ parents,
+    int32_t* __restrict__ off, int32_t* __restrict__ from, int32_t* __restrict__ to) {
+  __shared__ int waves[kBook / 64];
+  for (int i = threadIdx.x; i < pg.rows; i += kBook) {
+    named[i] = INT_MAX;
+    parents[i] = 0;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kBook) {
+    if ((unsigned)child[i] < (unsigned)pg.rows) atomicMin(&named[child[i]], i);
+    if ((unsigned)parent[i] < (unsigned)pg.rows) atomicOr(&parents[parent[i]], 1);
+  }
+  __syncthreads();
+  int total = 0;
+  for (int base = 0; base < n; base += kBook) {
+    const int i = base + threadIdx.x;
+    int need = 0;
+    if (i < n) {
+      const int c = child[i], p = parent[i];
+      bool good = (unsigned)c < (unsigned)pg.rows && (unsigned)p < (unsigned)pg.rows;
+      good = good && named[c] == i && !parents[c] && pg.held[c] <= 0;
+      int old = -1;
+      if (good) {
+        const int held = clamp_int(pg.held[p], 0, pg.width);
+        const int length = max(pg.length[p], 0);
+        const int full = length / pg.page_size;
+        if (length % pg.page_size && full < held) {
+          need = 1;
+          old = pg.table[(int64_t)p * pg.width + full];
+          if ((unsigned)old >= (unsigned)pg.pages) old = -1;
+        }
+      }
+      ok[i] = good;
+      from[i] = old;
+      to[i] = need ? 0 : -1;
+    }
+    int all;
+    const int end = scan_block(need, waves, &all);
+    if (i < n) off[i] = total + end - need;
+    total += all;
+  }
+  const int found = total ? min(count_free(pg.ref, pg.pages, total, waves), total) : 0;
+  __syncthreads();
+  give_free(pg.ref, pg.pages, found, waves, [&](int rank, int p) {
+    to[owner_of(off, n, rank)] = p;
+  });
+  for (int i = threadIdx.x; i < n; i += kBook)
+    if (to[i] >= 0 && off[i] >= found) {  // no page left for it
+      ok[i] = 0;
+      to[i] = -1;
+    }
+  __syncthreads();
+  const int lane = threadIdx.x & 63;
+  for (int i = threadIdx.x >> 6; i < n; i += kBook / 64) {
+    if (!ok[i]) continue;
+    const int p = parent[i], c = child[i];
+    const int held = clamp_int(pg.held[p], 0, pg.width);
+    const int length = max(pg.length[p], 0);
+    const int full = min(length / pg.page_size, held);
+    const int32_t* tp = pg.table + (int64_t)p * pg.width;
+    int32_t* tc = pg.table + (int64_t)c * pg.width;
+    for (int j = lane; j < full; j += 64) {
+      const int page = tp[j];
+      tc[j] = page;
+      if ((unsigned)page < (unsigned)pg.pages) atomicAdd(&pg.ref[page], 1);
+    }
+    if (lane == 0) {
+      const int own = to[i] >= 0;
+      if (own) tc[full] = to[i];
+      pg.held[c] = full + own;
+      pg.length[c] = own ? length : full * pg.page_size;
+    }
+  }
+}
+
+// The strided places of one page's 16-byte pieces.
+struct PageShape {
+  int64_t layer_stride, page_stride;
+  int64_t outer_stride, inner_stride;  // of the two of slots and heads
+  int inner, per;                      // inner count; pieces per head and slot
+  int pieces;                          // of a page
+  int pages, layers;
+};
+
+typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
+
+// One work-group per kCopy pieces of a page, layer and tensor. DENSE: a page
+// is one run of bytes.
+constexpr int kCopyPer = 4;
+constexpr int kCopy = 256 * kCopyPer;
+
+template <bool DENSE>
+__global__ __launch_bounds__(256) void cache_copy(uint16_t* __restrict__ k,
+                                                  uint16_t* __restrict__ v, const PageShape s,
+                                                  const int32_t* __restrict__ src,
+                                                  const int32_t* __restrict__ dst) {
+  const int i = blockIdx.y;
+  const int from = src[i], to = dst[i];
+  if ((unsigned)from >= (unsigned)s.pages || (unsigned)to >= (unsigned)s.pages || from == to)
+    return;
+  uint16_t* base = (blockIdx.z & 1 ? v : k) + (int64_t)(blockIdx.z >> 1) * s.layer_stride;
+  const uint16_t* a = base + (int64_t)from * s.page_stride;
+  uint16_t* b = base + (int64_t)to * s.page_stride;
+  const int p0 = blockIdx.x * kCopy + threadIdx.x;
+  u32x4 r[kCopyPer];
+  int64_t at[kCopyPer];
+#pragma unroll
+  for (int j = 0; j < kCopyPer; ++j) {
+    const int p = p0 + j * 256;
+    if (DENSE) {
+      at[j] = (int64_t)p * 8;
+    } else {
+      const int c = p % s.per, t = p / s.per;
+      at[j] = (int64_t)(t / s.inner) * s.outer_stride + (int64_t)(t % s.inner) * s.inner_stride +
+              c * 8;
+    }
+    if (p < s.pieces) r[j] = *reinterpret_cast<const u32x4*>(a + at[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < kCopyPer; ++j)
+    if (p0 + j * 256 < s.pieces) *reinterpret_cast<u32x4*>(b + at[j]) = r[j];
+}
+
+// One work-group per sequence and 256 of the columns (layer, tensor, head,
+// 16-byte piece); each thread walks its column's kept rows upwards. The r-th
+// kept row moves to place r, at or below its own, so a run of rows that is
+// read before it is written never loses a later row.
+constexpr int kRun = 8;
+
+__global__ __launch_bounds__(256) void cache_compact(const vqv_cache c, const vqv_seqs s,
+                                                     const int32_t* __restrict__ keep,
+                                                     int32_t* __restrict__ new_len) {
+  __shared__ int64_t from[256], to[256];
+  __shared__ int waves[4];
+  const int b = blockIdx.y;
+  const int first = max(s.row_start[b], 0), next = min(s.row_start[b + 1], s.n_rows);
+  const int n = max(next - first, 0);
+  const int kv = s.kv_len[b];
+  const int p0 = kv - n;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+
+  const int per = c.dim >> 3;
+  const int cols = c.layers * 2 * c.kv_heads * per;
+  const int col = blockIdx.x * 256 + threadIdx.x;
+  const int piece = col % per, head = col / per % c.kv_heads;
+  const int plane = col / per / c.kv_heads;
+  uint16_t* base = static_cast<uint16_t*>(plane & 1 ? c.v : c.k) +
+                   (int64_t)(plane >> 1) * c.layer_stride + (int64_t)head * c.head_stride +
+                   piece * 8;
+
+  int done = 0;  // kept rows of earlier runs of 256
+  for (int i0 = 0; i0 < n; i0 += 256) {
+    const int i = i0 + threadIdx.x;
+    const bool kept = i < n && keep[first + i] != 0;
+    const unsigned long long m = __ballot(kept);
+    __syncthreads();
+    if (lane == 0) waves[wave] = __popcll(m);
+    __syncthreads();
+    int rank = __popcll(m & ((1ull << lane) - 1)), all = 0;
+    for (int w = 0; w < 4; ++w) {
+      rank += w < wave ? waves[w] : 0;
+      all += waves[w];
+    }
+    if (kept) {
+      const int t = p0 + i, d = p0 + done + rank;
+      const int tp = page_of(s, b, t, c.page_size, c.pages);
+      const int dp = page_of(s, b, d, c.page_size, c.pages);
+      const bool move = t != d && tp >= 0 && dp >= 0;
+      from[rank] = move ? (int64_t)tp * c.page_stride + (int64_t)(t % c.page_size) * c.slot_stride
+                        : -1;
+      to[rank] = move ? (int64_t)dp * c.page_stride + (int64_t)(d % c.page_size) * c.slot_stride
+                      : -1;
+    }
+    __syncthreads();
+    if (col < cols) {
+      for (int r0 = 0; r0 < all; r0 += kRun) {
+        u32x4 x[kRun];
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+          if (r0 + j < all && from[r0 + j] >= 0)
+            x[j] = *reinterpret_cast<const u32x4*>(base + from[r0 + j]);
+#pragma unroll
+        for (int j = 0; j < kRun; ++j)
+          if (r0 + j < all && from[r0 + j] >= 0)
+            *reinterpret_cast<u32x4*>(base + to[r0 + j]) = x[j];
+      }
+    }
+    done += all;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) new_len[b] = p0 + done;
+}
+
+hipError_t launch_copy(const vqv_cache& c, const int32_t* src, const int32_t* dst, int n,
+                       hipStream_t stream) {
+  PageShape s{};
+  s.layer_stride = c.layer_stride;
+  s.page_stride = c.page_stride;
+  const bool slots_inner = c.slot_stride <= c.head_stride;
+  s.inner = slots_inner ? c.page_size : c.kv_heads;
+  s.inner_stride = slots_inner ? c.slot_stride : c.head_stride;
+  s.outer_stride = slots_inner ? c.head_stride : c.slot_stride;
+  const int outer = slots_inner ? c.kv_heads : c.page_size;
+  s.per = c.dim >> 3;
+  s.pieces = outer * s.inner * s.per;
+  s.pages = c.pages;
+  s.layers = c.layers;
+  const bool dense = (s.inner == 1 || s.inner_stride == c.dim) &&
+                     (outer == 1 || s.outer_stride == (int64_t)s.inner * c.dim);
+  // The grid's y holds 65535 pairs at a time.
+  for (int i = 0; i < n; i += 65535) {
+    const dim3 grid((s.pieces + kCopy - 1) / kCopy, n - i < 65535 ? n - i : 65535, c.layers * 2);
+    if (dense)
+      hipLaunchKernelGGL(cache_copy<true>, grid, dim3(256), 0, stream,
+                         static_cast<uint16_t*>(c.k), static_cast<uint16_t*>(c.v), s, src + i,
+                         dst + i);
+    else
+      hipLaunchKernelGGL(cache_copy<false>, grid, dim3(256), 0, stream,
+                         static_cast<uint16_t*>(c.k), static_cast<uint16_t*>(c.v), s, src + i,
+                         dst + i);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_cache_copy(const vqv_cache& cache, const int32_t* src, const int32_t* dst,
+                             int n, hipStream_t stream) {
+  return launch_copy(cache, src, dst, n, stream);
+}
+
+hipError_t launch_cache_trim(const vqv_pages& pages, const int32_t* keep_len, const int32_t* rows,
+                             int n, hipStream_t stream) {
+  hipLaunchKernelGGL(cache_trim, dim3(n), dim3(64), 0, stream, pages, keep_len, rows);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_reserve(const vqv_pages& pages, const int32_t* goal_len, int n,
+                                int32_t* ok, int32_t* scratch, hipStream_t stream) {
+  hipLaunchKernelGGL(cache_reserve, dim3(1), dim3(kBook), 0, stream, pages, goal_len, n, ok,
+                     scratch);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_fork(const vqv_cache& cache, const vqv_pages& pages,
+                             const int32_t* parent, const int32_t* child, int n, int32_t* ok,
+                             int32_t* scratch, hipStream_t stream) {
+  const int64_t r = pages.rows;
+  int32_t *named = scratch, *parents = scratch + r, *off = scratch + 2 * r;
+  int32_t *from = scratch + 3 * r, *to = scratch + 4 * r;
+  hipLaunchKernelGGL(cache_fork_book, dim3(1), dim3(kBook), 0, stream, pages, parent, child, n,
+                     ok, named, parents, off, from, to);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return launch_copy(cache, from, to, n, stream);
+}
+
+hipError_t launch_cache_compact(const vqv_cache& cache, const vqv_seqs& seqs, const int32_t* keep,
+                                int32_t* new_len, hipStream_t stream) {
+  const int cols = cache.layers * 2 * cache.kv_heads * (cache.dim >> 3);
+  hipLaunchKernelGGL(cache_compact, dim3((cols + 255) / 256, seqs.n_seqs), dim3(256), 0, stream,
+                     cache, seqs, keep, new_len);
+  return hipGetLastError();
+}
+
+}  // namespace vqv
