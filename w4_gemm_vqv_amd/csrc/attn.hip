@@ -38,6 +38,8 @@ typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 
+constexpr unsigned kNoPlace = ~0u;
+
 struct AttnArgs {
   const void* q;
   void* out;
@@ -45,6 +47,8 @@ struct AttnArgs {
   const void* v;
   vqv_seqs seqs;
   int page_size, pages, kv_heads, group;  // group: query heads per key head
+  unsigned page_mul;                      // t / page_size = (t * page_mul) >> 32 >> page_shift
+  int page_shift;                         // (page_mul 0: page_size is 1)
   unsigned page_units, slot_units, head_units;  // strides in 16-byte units
   float scale_log2;
   int window, sinks;
@@ -92,24 +96,38 @@ __device__ __forceinline__ unsigned not_finite(unsigned w) {
   return ((w & (e | e << 16)) + (low | low << 16)) & 0x80008000u;
 }
 
-// Takes the infinities and NaN out of the values `va` (tokens in a lane's
-// order, `seen` their bits for the lane's query row) and adds what they come
-// to: where a row sees one, the infinity, or both (NaN). Which rows see one is
-// a product of zeros and ones.
+// Values with 0 in the place of infinities and NaN.
 template <typename T>
-__device__ void add_not_finite(s16x8& va, unsigned seen, f32x16& o) {
-  constexpr unsigned e = Bits<T>::exponent;
-  s16x8 up = {}, down = {}, see = {};
+__device__ __forceinline__ s16x8 finite(s16x8 v) {
+  u32x4 w = __builtin_bit_cast(u32x4, v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const unsigned w = (unsigned short)va[i];
-    const bool out = (w & e) == e, nan = out && (w & 0x7FFFu) != e;
-    up[i] = out && (nan || !(w & 0x8000u)) ? Bits<T>::one : 0;
-    down[i] = out && (nan || (w & 0x8000u)) ? Bits<T>::one : 0;
-    see[i] = seen >> i & 1u ? Bits<T>::one : 0;
-    va[i] = out ? 0 : va[i];
+  for (int i = 0; i < 4; ++i) w[i] &= ~((not_finite<T>(w[i]) >> 15) * 0xFFFFu);
+  return __builtin_bit_cast(s16x8, w);
+}
+
+// Adds to o what the infinities and NaN of a column come to: where a row sees
+// one, the infinity, or both (NaN). Which rows see one is a product of zeros
+// and ones, over the 16-token steps of a block; `seen` holds a lane's bits of
+// the tokens that its query row sees, 8 to a step.
+template <typename T, int STEPS, typename F>
+__device__ __forceinline__ void add_not_finite(F values, unsigned seen, f32x16& o) {
+  constexpr unsigned e = Bits<T>::exponent;
+  f32x16 a = {}, b = {};
+#pragma unroll 1
+  for (int u = 0; u < STEPS; ++u) {
+    const s16x8 v = values(u);
+    s16x8 up = {}, down = {}, see = {};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned w = (unsigned short)v[i];
+      const bool out = (w & e) == e, nan = out && (w & 0x7FFFu) != e;
+      up[i] = out && (nan || !(w & 0x8000u)) ? Bits<T>::one : 0;
+      down[i] = out && (nan || (w & 0x8000u)) ? Bits<T>::one : 0;
+      see[i] = seen >> (8 * u + i) & 1u ? Bits<T>::one : 0;
+    }
+    a = mfma<T>(up, see, a);
+    b = mfma<T>(down, see, b);
   }
-  const f32x16 a = mfma<T>(up, see, f32x16{}), b = mfma<T>(down, see, f32x16{});
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     if (a[i] != 0.0f) o[i] += __builtin_inff();
@@ -132,6 +150,34 @@ __device__ __forceinline__ int v_piece(int row, int c) {
   if (DC % 16 == 0) return c ^ ((row & 3) << 2);
   if (DC % 8 == 0) return c ^ ((row >> 1 & 1) << 2);
   return c;
+}
+
+__device__ __forceinline__ int page_index(const AttnArgs& a, int t) {
+  return a.page_mul ? (int)(__umulhi((unsigned)t, a.page_mul) >> a.page_shift) : t;
+}
+
+// 16 bytes per active lane from global memory to LDS at `lds` (uniform) + 16 *
+// lane, without registers between. It is an instruction of its own kind to the
+// compiler, which would otherwise wait for it before every LDS read: staged()
+// waits for it. The no-op covers the write of m0, which nothing
+// else here uses.
+__device__ __forceinline__ void load_to_lds(const void* from, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds), "v"(from)
+               : "memory");
+}
+// Everything this wave has asked for is there, and then every wave's.
+__device__ __forceinline__ void staged() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+__device__ __forceinline__ float max_of_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // The tokens that the rows of a tile see, as blocks of BT tokens: `sink`
@@ -163,17 +209,18 @@ __device__ __forceinline__ int blocks_of_split(const AttnArgs& a, int all) {
 }
 
 template <typename T, int D, int MW, int KW, int KT>
-__global__ __launch_bounds__(MW * KW * 64) void paged_attn(const AttnArgs a) {
+__global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(const AttnArgs a) {
   constexpr int NW = MW * KW, BT = KW * KT, DC = D / 8, DS = D / 16, DB = (D + 31) / 32;
-  constexpr int NT = NW * 64;
-  constexpr int PIECES = BT * DC;                    // of the keys of a block
-  constexpr int LOADS = (PIECES + NT - 1) / NT;      // per thread
+  constexpr int GROUPS = BT * DC / 64;               // of 64 pieces: a wave's access
+  constexpr int LOADS = (GROUPS + NW - 1) / NW;      // per wave, of keys and of values
   constexpr int SUB = KT / 32;
   constexpr int STAGE = BT * D;                      // values of K (or V) of a block
-  // One more row: the last column block of V reads past its row where D is
-  // not a multiple of 32 (the results are not used).
-  constexpr int VSTAGE = STAGE + 32;
+  // Where D is not a multiple of 32 the last column block of V reads past its
+  // row, at the end past its stage (the results are not used).
+  constexpr int VSTAGE = STAGE + (D % 32 ? 32 : 0);
   __shared__ __align__(16) uint16_t lds[2 * (STAGE + VSTAGE)];
+  __shared__ unsigned places[2][BT];
+  __shared__ int holes;  // not 0: a page was missing
 
   const int h = blockIdx.x % a.kv_heads;
   const int b = blockIdx.x / a.kv_heads % a.seqs.n_seqs;
@@ -219,52 +266,79 @@ __global__ __launch_bounds__(MW * KW * 64) void paged_attn(const AttnArgs a) {
   for (int d = 0; d < DB; ++d) o[d] = f32x16{};
   float mx = -__builtin_inff(), sum = 0.0f;
 
-  u32x4 kr[LOADS], vr[LOADS];
   const auto base_of = [&](int j) {
     return (j < blocks.sink ? j : blocks.first + j - blocks.sink) * BT;
   };
-  const auto load = [&](int j) {
-    const int t0 = base_of(j);
-#pragma unroll
-    for (int x = 0; x < LOADS; ++x) {
-      const int p = x * NT + threadIdx.x;
-      const int t = t0 + p / DC, c = p % DC;
-      kr[x] = u32x4{};
-      vr[x] = u32x4{};
-      if (p < PIECES && t < kv_len) {
-        const int page = page_of(a.seqs, b, t, a.page_size, a.pages);
-        if (page >= 0) {
-          const uint64_t u = (uint64_t)page * a.page_units +
-                             (uint64_t)(t % a.page_size) * a.slot_units +
-                             (uint64_t)h * a.head_units + c;
-          kr[x] = static_cast<const u32x4*>(a.k)[u];
-          vr[x] = static_cast<const u32x4*>(a.v)[u];
-        }
-      }
+
+  // A block's tokens are looked up by as many threads, two blocks ahead of
+  // their loads (the entry of the table is asked for three ahead): places[]
+  // holds a token's place in the cache in 16-byte units, or kNoPlace.
+  const char* kbase = static_cast<const char*>(a.k) + (uint64_t)h * a.head_units * 16;
+  const char* vbase = static_cast<const char*>(a.v) + (uint64_t)h * a.head_units * 16;
+  const int32_t* table = a.seqs.table + (int64_t)b * a.seqs.table_stride;
+  int entry = -1;
+  const auto ask = [&](int j) {
+    entry = -1;
+    if ((int)threadIdx.x < BT && j < j1) {
+      const int t = base_of(j) + threadIdx.x, i = page_index(a, t);
+      if (t < kv_len && i < a.seqs.table_width) entry = table[i];
     }
   };
-  const auto store = [&](int buf) {
-    uint16_t* ks = lds + buf * (STAGE + VSTAGE);
-    uint16_t* vs = ks + STAGE;
+  const auto look_up = [&](int j) {
+    if ((int)threadIdx.x < BT && j < j1) {
+      const int t = base_of(j) + threadIdx.x;
+      unsigned place = kNoPlace;
+      if ((unsigned)entry < (unsigned)a.pages)
+        place = (unsigned)entry * a.page_units +
+                (unsigned)(t - page_index(a, t) * a.page_size) * a.slot_units;
+      else if (t < kv_len)
+        holes = 1;
+      places[(j - j0) & 1][threadIdx.x] = place;
+    }
+  };
+  // Piece p of a block's keys goes to LDS place p; it is piece k_piece(t, p %
+  // DC) of token t = p / DC, and likewise for the values. Values of tokens
+  // that are none are zeros, for the product; their scores are masked.
+  const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  const auto load = [&](int j, int buf) {
+    const unsigned kl = lds0 + buf * (STAGE + VSTAGE) * 2, vl = kl + STAGE * 2;
+    uint16_t* vs = lds + buf * (STAGE + VSTAGE) + STAGE;
 #pragma unroll
     for (int x = 0; x < LOADS; ++x) {
-      const int p = x * NT + threadIdx.x;
-      const int t = p / DC, c = p % DC;
-      if (p < PIECES) {
-        *reinterpret_cast<u32x4*>(ks + t * D + k_piece<DC>(t, c) * 8) = kr[x];
-        *reinterpret_cast<u32x4*>(vs + t * D + v_piece<DC>(t, c) * 8) = vr[x];
+      const int g0 = x * NW + wave;
+      if (GROUPS % NW && g0 >= GROUPS) continue;
+      const int p = g0 * 64 + lane, t = p / DC, c = p % DC;
+      const unsigned place = places[(j - j0) & 1][t];
+      const unsigned kb = __builtin_amdgcn_readfirstlane(kl + g0 * 1024);
+      const unsigned vb = __builtin_amdgcn_readfirstlane(vl + g0 * 1024);
+      if (place != kNoPlace) {
+        load_to_lds(kbase + ((uint64_t)place + k_piece<DC>(t, c)) * 16, kb);
+        load_to_lds(vbase + ((uint64_t)place + v_piece<DC>(t, c)) * 16, vb);
+      } else {
+        *reinterpret_cast<u32x4*>(vs + p * 8) = u32x4{};
       }
     }
   };
 
-  if (j0 < j1) {
-    load(j0);
-    store(0);
-  }
+  if (threadIdx.x == 0) holes = 0;
+  __syncthreads();
+  ask(j0);
+  look_up(j0);
+  ask(j0 + 1);
+  look_up(j0 + 1);
+  __syncthreads();
+  if (j0 < j1) load(j0, 0);
+  ask(j0 + 2);
   for (int j = j0; j < j1; ++j) {
     const int buf = (j - j0) & 1;
-    if (j + 1 < j1) load(j + 1);
-    __syncthreads();
+    // Block j is there for all, and all are done with the other buffer.
+    staged();
+    if (j + 1 < j1) {
+      asm volatile("" : "+v"(entry));  // the wait for it is over: not after the loads
+      load(j + 1, 1 - buf);
+      look_up(j + 2);
+      ask(j + 3);
+    }
     const uint16_t* ks = lds + buf * (STAGE + VSTAGE) + kw * KT * D;
     const uint16_t* vs = lds + buf * (STAGE + VSTAGE) + STAGE + kw * KT * D;
     const int t0 = base_of(j) + kw * KT;
@@ -284,32 +358,34 @@ __global__ __launch_bounds__(MW * KW * 64) void paged_attn(const AttnArgs a) {
     // Hidden tokens, and those without a page. Where every row sees every token
     // there is nothing to mask.
     bool full = t0 + KT - 1 <= p0 && (a.window == 0 || t0 > p1 - a.window);
-    unsigned paged[SUB], seen = 0;
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      const int tk = t0 + 32 * u + ql;
-      paged[u] =
-          (unsigned)__ballot(tk < kv_len && page_of(a.seqs, b, tk, a.page_size, a.pages) >= 0);
-      full = full && paged[u] == ~0u;
-    }
+    const bool whole = *const_cast<volatile int*>(&holes) == 0;
+    full = full && t0 + KT <= kv_len && whole;
+    unsigned seen = 0;
     if (!full) {
 #pragma unroll
-      for (int u = 0; u < SUB; ++u)
+      for (int u = 0; u < SUB; ++u) {
+        unsigned paged = ~0u;
+        if (!whole) {
+          const int tk = t0 + 32 * u + ql;
+          paged = (unsigned)__ballot(
+              tk < kv_len && page_of(a.seqs, b, tk, a.page_size, a.pages) >= 0);
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int k = 8 * (i / 4) + 4 * half + (i & 3), t = t0 + 32 * u + k;
-          bool see = t <= pos && (paged[u] >> k & 1u);
+          bool see = t <= pos && t < kv_len && (paged >> k & 1u);
           if (a.window > 0) see = see && (t > pos - a.window || t < a.sinks);
           s[u][i] = see ? s[u][i] : -__builtin_inff();
           seen |= (see ? 1u : 0u) << (16 * u + i);
         }
+      }
     }
     float top = mx;
 #pragma unroll
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = max_of_halves(top);
     const float shift = top == -__builtin_inff() ? 0.0f : top * a.scale_log2;
     const float back = mx == -__builtin_inff() ? 0.0f
                                                : __builtin_amdgcn_exp2f(mx * a.scale_log2 - shift);
@@ -340,31 +416,41 @@ __global__ __launch_bounds__(MW * KW * 64) void paged_attn(const AttnArgs a) {
       }
       bad = __ballot(found != 0) != 0;
     }
+    const auto values = [&](int u, int d) {
+      // Lane l of 16 reads 4 columns of token l / 4; it gets 4 tokens of column l % 16.
+      s16x4 vf[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int row = 16 * u + 8 * y + 4 * half + (lane >> 2 & 3);
+        const int col = 32 * d + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+        const uint16_t* p = vs + row * D + v_piece<DC>(row, col >> 3) * 8 + (col & 7);
+        vf[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)p);
+      }
+      return __builtin_shufflevector(vf[0], vf[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    };
+    s16x8 pf[2 * SUB];
 #pragma unroll
     for (int u = 0; u < 2 * SUB; ++u) {
       u32x4 pw;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         pw[i] = pack2<T>(s[u / 2][8 * (u & 1) + 2 * i], s[u / 2][8 * (u & 1) + 2 * i + 1]);
-      const s16x8 pf = __builtin_bit_cast(s16x8, pw);
+      pf[u] = __builtin_bit_cast(s16x8, pw);
+    }
+    if (bad) {
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
-        // Lane l of 16 reads 4 columns of token l / 4; it gets 4 tokens of column l % 16.
-        s16x4 vf[2];
+        add_not_finite<T, 2 * SUB>([&](int u) { return values(u, d); }, seen, o[d]);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int row = 16 * u + 8 * y + 4 * half + (lane >> 2 & 3);
-          const int col = 32 * d + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
-          const uint16_t* p = vs + row * D + v_piece<DC>(row, col >> 3) * 8 + (col & 7);
-          vf[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4*)p);
-        }
-        s16x8 va = __builtin_shufflevector(vf[0], vf[1], 0, 1, 2, 3, 4, 5, 6, 7);
-        if (bad) add_not_finite<T>(va, seen >> (8 * u), o[d]);
-        o[d] = mfma<T>(va, pf, o[d]);
+        for (int u = 0; u < 2 * SUB; ++u) o[d] = mfma<T>(finite<T>(values(u, d)), pf[u], o[d]);
       }
+    } else {
+#pragma unroll
+      for (int u = 0; u < 2 * SUB; ++u)
+#pragma unroll
+        for (int d = 0; d < DB; ++d) o[d] = mfma<T>(values(u, d), pf[u], o[d]);
     }
-    if (j + 1 < j1) store(1 - buf);
   }
   sum += __shfl_xor(sum, 32);
 
@@ -564,6 +650,14 @@ hipError_t launch_paged_attn(const void* q, const vqv_cache& c, int layer, const
   a.seqs = seqs;
   a.page_size = c.page_size;
   a.pages = c.pages;
+  a.page_mul = 0;
+  a.page_shift = 0;
+  if (c.page_size > 1) {
+    // ceil(2^(32 + shift) / page_size) with 2^shift < page_size <= 2^(shift + 1): exact for
+    // tokens below 2^31.
+    while ((2ll << a.page_shift) < c.page_size) ++a.page_shift;
+    a.page_mul = (unsigned)(((1ull << (32 + a.page_shift)) + c.page_size - 1) / c.page_size);
+  }
   a.kv_heads = c.kv_heads;
   a.group = heads / c.kv_heads;
   a.page_units = (unsigned)(c.page_stride >> 3);
