@@ -23,6 +23,8 @@
 // instruction's input: an error of at most half a step of each weight, which
 // the sum over tokens averages.
 
+#include <limits.h>
+
 #include "round_common.h"
 #include "round_internal.h"
 
@@ -39,6 +41,7 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 constexpr unsigned kNoPlace = ~0u;
+constexpr float kSlack = 8.0f;
 
 struct AttnArgs {
   const void* q;
@@ -174,6 +177,25 @@ __device__ __forceinline__ void staged() {
   asm volatile("" ::: "memory");
 }
 
+// The order of a run of N matrix instructions that each take READS LDS reads:
+// the reads of AHEAD of them go first, and then one's with each.
+template <int N, int READS, int AHEAD>
+__device__ __forceinline__ void pipelined() {
+  constexpr int ahead = N < AHEAD ? N : AHEAD;
+  __builtin_amdgcn_sched_group_barrier(0x100, READS * ahead, 0);
+#pragma unroll
+  for (int i = 0; i < N - ahead; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, ahead, 0);
+}
+
+// exp2((x - top) * scale), 0 where x is -inf (also when both are).
+__device__ __forceinline__ float exp_of(float x, float top, float scale) {
+  return x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((x - top) * scale);
+}
+
 __device__ __forceinline__ float max_of_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
                                                   false);
@@ -219,7 +241,7 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
   // row, at the end past its stage (the results are not used).
   constexpr int VSTAGE = STAGE + (D % 32 ? 32 : 0);
   __shared__ __align__(16) uint16_t lds[2 * (STAGE + VSTAGE)];
-  __shared__ unsigned places[2][BT];
+  __shared__ unsigned places[4][BT];
   __shared__ int holes;  // not 0: a page was missing
 
   const int h = blockIdx.x % a.kv_heads;
@@ -293,7 +315,7 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
                 (unsigned)(t - page_index(a, t) * a.page_size) * a.slot_units;
       else if (t < kv_len)
         holes = 1;
-      places[(j - j0) & 1][threadIdx.x] = place;
+      places[(j - j0) & 3][threadIdx.x] = place;
     }
   };
   // Piece p of a block's keys goes to LDS place p; it is piece k_piece(t, p %
@@ -303,17 +325,26 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
   const auto load = [&](int j, int buf) {
     const unsigned kl = lds0 + buf * (STAGE + VSTAGE) * 2, vl = kl + STAGE * 2;
     uint16_t* vs = lds + buf * (STAGE + VSTAGE) + STAGE;
+    unsigned place[LOADS];
+    bool all = true;
+#pragma unroll
+    for (int x = 0; x < LOADS; ++x) {
+      const int g0 = x * NW + wave;
+      if (GROUPS % NW && g0 >= GROUPS) continue;
+      place[x] = places[(j - j0) & 3][(g0 * 64 + lane) / DC];
+      all = all && place[x] != kNoPlace;
+    }
+    const bool whole = __all(all);
 #pragma unroll
     for (int x = 0; x < LOADS; ++x) {
       const int g0 = x * NW + wave;
       if (GROUPS % NW && g0 >= GROUPS) continue;
       const int p = g0 * 64 + lane, t = p / DC, c = p % DC;
-      const unsigned place = places[(j - j0) & 1][t];
       const unsigned kb = __builtin_amdgcn_readfirstlane(kl + g0 * 1024);
       const unsigned vb = __builtin_amdgcn_readfirstlane(vl + g0 * 1024);
-      if (place != kNoPlace) {
-        load_to_lds(kbase + ((uint64_t)place + k_piece<DC>(t, c)) * 16, kb);
-        load_to_lds(vbase + ((uint64_t)place + v_piece<DC>(t, c)) * 16, vb);
+      if (whole || place[x] != kNoPlace) {
+        load_to_lds(kbase + (uint64_t)(place[x] + k_piece<DC>(t, c)) * 16, kb);
+        load_to_lds(vbase + (uint64_t)(place[x] + v_piece<DC>(t, c)) * 16, vb);
       } else {
         *reinterpret_cast<u32x4*>(vs + p * 8) = u32x4{};
       }
@@ -345,16 +376,16 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
 
     f32x16 s[SUB];
 #pragma unroll
-    for (int u = 0; u < SUB; ++u) {
-      s[u] = f32x16{};
+    for (int x = 0; x < DS; ++x) {
 #pragma unroll
-      for (int x = 0; x < DS; ++x) {
+      for (int u = 0; u < SUB; ++u) {
         const int row = 32 * u + ql;
         const s16x8 kf = *reinterpret_cast<const s16x8*>(
             ks + row * D + k_piece<DC>(row, 2 * x + half) * 8);
-        s[u] = mfma<T>(kf, qf[x], s[u]);
+        s[u] = mfma<T>(kf, qf[x], x ? s[u] : f32x16{});
       }
     }
+    pipelined<SUB * DS, 1, 4>();
     // Hidden tokens, and those without a page. Where every row sees every token
     // there is nothing to mask.
     bool full = t0 + KT - 1 <= p0 && (a.window == 0 || t0 > p1 - a.window);
@@ -362,35 +393,44 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
     full = full && t0 + KT <= kv_len && whole;
     unsigned seen = 0;
     if (!full) {
+      // Token t0 + 32 u + 8 (i / 4) + 4 half + i % 4, against the row's bounds.
+      const int hi = pos - t0 - 4 * half;
+      const int lo = a.window > 0 ? hi - a.window : INT_MIN;
+      const int sink = a.sinks - t0 - 4 * half;
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        unsigned paged = ~0u;
-        if (!whole) {
-          const int tk = t0 + 32 * u + ql;
-          paged = (unsigned)__ballot(
-              tk < kv_len && page_of(a.seqs, b, tk, a.page_size, a.pages) >= 0);
-        }
+        const unsigned paged =
+            (unsigned)__ballot(places[(j - j0) & 3][kw * KT + 32 * u + ql] != kNoPlace) >>
+            (4 * half);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const int k = 8 * (i / 4) + 4 * half + (i & 3), t = t0 + 32 * u + k;
-          bool see = t <= pos && t < kv_len && (paged >> k & 1u);
-          if (a.window > 0) see = see && (t > pos - a.window || t < a.sinks);
+          const int k = 8 * (i / 4) + (i & 3), r = 32 * u + k;
+          const bool see = r <= hi && (r > lo || r < sink) && (paged >> k & 1u);
           s[u][i] = see ? s[u][i] : -__builtin_inff();
           seen |= (see ? 1u : 0u) << (16 * u + i);
         }
       }
     }
-    float top = mx;
+    float top = s[0][0];
 #pragma unroll
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[u][i]);
     top = max_of_halves(top);
-    const float shift = top == -__builtin_inff() ? 0.0f : top * a.scale_log2;
-    const float back = mx == -__builtin_inff() ? 0.0f
-                                               : __builtin_amdgcn_exp2f(mx * a.scale_log2 - shift);
-    mx = top;
-    sum *= back;
+    // The maximum that weights are relative to follows the scores only when
+    // they pass it by 2^kSlack: a weight is then at most that, and the sums
+    // need no scaling in most blocks.
+    if (__any((top - mx) * a.scale_log2 > kSlack)) {
+      const float now = fmaxf(mx, top);
+      const float back = exp_of(mx, now, a.scale_log2);
+      mx = now;
+      sum *= back;
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] *= back;
+    }
+    const float shift = mx == -__builtin_inff() ? 0.0f : mx * a.scale_log2;
 #pragma unroll
     for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -398,10 +438,6 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
         s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], a.scale_log2, -shift));
         sum += s[u][i];
       }
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[d][i] *= back;
 
     // A hidden token's weight is 0, which an infinity or NaN of its values
     // would turn into NaN: where some rows do not see all tokens, such values
@@ -450,6 +486,7 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
       for (int u = 0; u < 2 * SUB; ++u)
 #pragma unroll
         for (int d = 0; d < DB; ++d) o[d] = mfma<T>(values(u, d), pf[u], o[d]);
+      pipelined<2 * SUB * DB, 2, 4>();
     }
   }
   sum += __shfl_xor(sum, 32);
@@ -475,9 +512,7 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
       if (kw < w) {
         const float om = mine[DB * 16 * 64], os = mine[(DB * 16 + 1) * 64];
         const float top = fmaxf(mx, om);
-        const float shift = top == -__builtin_inff() ? 0.0f : top * a.scale_log2;
-        const float fa = __builtin_amdgcn_exp2f(mx * a.scale_log2 - shift);
-        const float fb = __builtin_amdgcn_exp2f(om * a.scale_log2 - shift);
+        const float fa = exp_of(mx, top, a.scale_log2), fb = exp_of(om, top, a.scale_log2);
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -543,18 +578,31 @@ __global__ __launch_bounds__(64) void paged_attn_join(const AttnArgs a, int rows
   const int per_split = blocks_of_split(a, blocks.all);
   const int parts = (blocks.all + per_split - 1) / per_split;
   if (parts <= 1) return;  // written by the first kernel
+  // Lane l takes the maxima and sums of parts l, l + 64, ..; the weights of
+  // the parts then go from lane to lane.
   const int64_t at = (int64_t)blockIdx.x * a.splits;
+  const int lane = threadIdx.x, col = lane * 4;
   float top = -__builtin_inff();
-  for (int s = 0; s < parts; ++s) top = fmaxf(top, a.part_ml[2 * (at + s)]);
-  const float shift = top == -__builtin_inff() ? 0.0f : top * a.scale_log2;
-  const int col = threadIdx.x * 4;
+  for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_ml[2 * (at + s)]);
+#pragma unroll
+  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
   f32x4 o = {};
   float sum = 0.0f;
-  for (int s = 0; s < parts; ++s) {
-    const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (at + s)] * a.scale_log2 - shift);
-    sum += f * a.part_ml[2 * (at + s) + 1];
-    if (col < D) o += f * *reinterpret_cast<const f32x4*>(a.part + (at + s) * D + col);
+  for (int s0 = 0; s0 < parts; s0 += 64) {
+    float w = 0.0f;
+    if (s0 + lane < parts) {
+      w = exp_of(a.part_ml[2 * (at + s0 + lane)], top, a.scale_log2);
+      sum += w * a.part_ml[2 * (at + s0 + lane) + 1];
+    }
+    const int n = min(parts - s0, 64);
+#pragma unroll 8
+    for (int s = 0; s < n; ++s) {
+      const float f = __shfl(w, s);
+      if (col < D) o += f * *reinterpret_cast<const f32x4*>(a.part + (at + s0 + s) * D + col);
+    }
   }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   if (col < D) {
     const u32x2 w = {pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv)};
