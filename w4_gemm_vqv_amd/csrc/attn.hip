@@ -558,10 +558,12 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
   }
 }
 
-// Joins the partial sums of a (row, head): one wave, 4 columns per lane.
-template <typename T, int BT>
-__global__ __launch_bounds__(64) void paged_attn_join(const AttnArgs a, int rows_per_tile,
-                                                      int D) {
+// Joins the partial sums of a (row, head): one work-group, 4 columns per
+// thread, so that 1024 / D (rounded down) parts are read at the same time.
+template <typename T, int D, int BT>
+__global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a, int rows_per_tile) {
+  constexpr int COLS = D / 4, SETS = 256 / COLS;
+  __shared__ f32x4 sums[SETS][COLS];
   const int heads = a.kv_heads * a.group;
   const int r = blockIdx.x / heads, head = blockIdx.x % heads;
   const int b = seq_of_row(a.seqs.row_start, a.seqs.n_seqs, r);
@@ -578,35 +580,35 @@ __global__ __launch_bounds__(64) void paged_attn_join(const AttnArgs a, int rows
   const int per_split = blocks_of_split(a, blocks.all);
   const int parts = (blocks.all + per_split - 1) / per_split;
   if (parts <= 1) return;  // written by the first kernel
-  // Lane l takes the maxima and sums of parts l, l + 64, ..; the weights of
-  // the parts then go from lane to lane.
   const int64_t at = (int64_t)blockIdx.x * a.splits;
-  const int lane = threadIdx.x, col = lane * 4;
+  const float* ml = a.part_ml + 2 * at;
+  const int lane = threadIdx.x & 63;
   float top = -__builtin_inff();
-  for (int s = lane; s < parts; s += 64) top = fmaxf(top, a.part_ml[2 * (at + s)]);
+  for (int s = lane; s < parts; s += 64) top = fmaxf(top, ml[2 * s]);
 #pragma unroll
   for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  f32x4 o = {};
   float sum = 0.0f;
-  for (int s0 = 0; s0 < parts; s0 += 64) {
-    float w = 0.0f;
-    if (s0 + lane < parts) {
-      w = exp_of(a.part_ml[2 * (at + s0 + lane)], top, a.scale_log2);
-      sum += w * a.part_ml[2 * (at + s0 + lane) + 1];
-    }
-    const int n = min(parts - s0, 64);
-#pragma unroll 8
-    for (int s = 0; s < n; ++s) {
-      const float f = __shfl(w, s);
-      if (col < D) o += f * *reinterpret_cast<const f32x4*>(a.part + (at + s0 + s) * D + col);
-    }
-  }
+  for (int s = lane; s < parts; s += 64) sum += exp_of(ml[2 * s], top, a.scale_log2) * ml[2 * s + 1];
 #pragma unroll
   for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  if (col < D) {
+
+  const int set = threadIdx.x / COLS, col = threadIdx.x % COLS;
+  f32x4 o = {};
+  if (set < SETS) {
+    const float* part = a.part + at * D + 4 * col;
+#pragma unroll 4
+    for (int s = set; s < parts; s += SETS)
+      o += exp_of(ml[2 * s], top, a.scale_log2) *
+           *reinterpret_cast<const f32x4*>(part + (int64_t)s * D);
+    sums[set][col] = o;
+  }
+  __syncthreads();
+  if (set == 0) {
+    for (int x = 1; x < SETS; ++x) o += sums[x][col];
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const u32x2 w = {pack2<T>(o[0] * inv, o[1] * inv), pack2<T>(o[2] * inv, o[3] * inv)};
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (int64_t)blockIdx.x * D + col) = w;
+    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + (int64_t)blockIdx.x * D + 4 * col) =
+        w;
   }
 }
 
@@ -617,18 +619,22 @@ hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
                      stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((paged_attn_join<T, KW * KT>),
-                     dim3((unsigned)(a.seqs.n_rows * a.kv_heads * a.group)), dim3(64), 0, stream,
-                     a, MW * 32, D);
+  hipLaunchKernelGGL((paged_attn_join<T, D, KW * KT>),
+                     dim3((unsigned)(a.seqs.n_rows * a.kv_heads * a.group)), dim3(256), 0, stream,
+                     a, MW * 32);
   return hipGetLastError();
 }
 
+// Waves that split the tokens of a block while there are few query rows. Two
+// work-groups then fit a CU's LDS, and one's loads fill the other's pauses.
+constexpr int token_waves(int dim) { return dim <= 64 ? 4 : dim <= 128 ? 2 : 1; }
+
 template <typename T, int D>
 hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
-  constexpr bool wide = D > 128;
-  if (p.mw == 4) return launch_shape<T, D, 4, 1, wide ? 32 : 64>(a, stream);
-  if (p.mw == 2) return launch_shape<T, D, 2, 2, 32>(a, stream);
-  return launch_shape<T, D, 1, wide ? 2 : 4, 32>(a, stream);
+  constexpr int kw = token_waves(D);
+  if (p.mw == 4) return launch_shape<T, D, 4, 1, D <= 128 ? 64 : 32>(a, stream);
+  if (p.mw == 2) return launch_shape<T, D, 2, kw < 2 ? kw : 2, 32>(a, stream);
+  return launch_shape<T, D, 1, kw, 32>(a, stream);
 }
 
 template <typename T>
@@ -652,12 +658,12 @@ bool attn_dim_supported(int dim) {
 }
 
 AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window, int sinks) {
-  const bool wide = c.dim > 128;
   const int64_t m = (int64_t)(s.max_rows < s.n_rows ? s.max_rows : s.n_rows) * (heads / c.kv_heads);
+  const int kw = token_waves(c.dim);
   AttnPlan p;
   p.mw = m <= 32 ? 1 : m <= 64 ? 2 : 4;
-  p.kw = p.mw == 4 ? 1 : p.mw == 2 ? 2 : wide ? 2 : 4;
-  p.kt = p.mw == 4 && !wide ? 64 : 32;
+  p.kw = p.mw == 4 ? 1 : p.mw == 2 && kw > 2 ? 2 : kw;
+  p.kt = p.mw == 4 && c.dim <= 128 ? 64 : 32;
   p.tiles = ceil_div(m < 1 ? 1 : m, 32 * p.mw);
   const int bt = p.kw * p.kt;
   // The most blocks that a tile's rows see.
@@ -669,15 +675,26 @@ AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window,
     tokens = seen < tokens ? seen : tokens;
   }
   const int blocks = ceil_div(tokens < 1 ? 1 : tokens, bt);
-  // Work-groups wanted: several rounds over the CUs where the tokens are the
-  // work (their lengths differ), one round of two per CU for full tiles.
   const int64_t base = (int64_t)c.kv_heads * s.n_seqs * p.tiles;
-  const int64_t want = p.mw == 4 ? 512 : 2048;
-  const int least = p.mw == 4 ? 4 : 1;  // blocks of a split
-  int64_t splits = want / (base < 1 ? 1 : base);
-  if (splits < 1) splits = 1;
-  p.split_blocks = ceil_div(blocks, splits);
-  if (p.split_blocks < least) p.split_blocks = least;
+  // Blocks of a split. Full tiles: two work-groups for each of the 256 CUs in
+  // one round, splits of 4 blocks at least. Few query rows: one work-group per
+  // CU while that leaves splits of 16 blocks or fewer (a block of 8 rows over
+  // 4096 tokens: 14.6 us, with two per CU 16.3, one for two CUs 16.7); then
+  // splits of 16 or more, in 16 rounds as lengths differ (48 ragged sequences:
+  // 376 us, in 8 rounds 403, in 4 455), but in two where a window makes them
+  // alike (74 us, in 4 rounds 82).
+  int64_t per;
+  if (p.mw == 4) {
+    per = ceil_div(blocks * base, 512);
+    if (per < 4) per = 4;
+  } else {
+    per = ceil_div(blocks * base, 256);
+    if (per > 16) {
+      per = ceil_div(blocks * base, window > 0 ? 512 : 4096);
+      if (per < 16) per = 16;
+    }
+  }
+  p.split_blocks = per < blocks ? (int)per : blocks;
   p.splits = ceil_div(blocks, p.split_blocks);
   return p;
 }
