@@ -1,13 +1,22 @@
 // Attention of new rows over a paged cache (vqv_paged_attn).
 //
 // The query rows of a sequence that share a key head, (row, head) pairs with
-// the head fastest, are cut into tiles of 32 per wave; a work-group of MW x KW
-// waves walks over the visible tokens in blocks of KW * KT, staged in LDS, so
-// that every wave reads each key and value once from there whatever the page
-// size and layout. Wave (mw, kw) takes query tile mw and the kw-th KT tokens
-// of each block. With few query rows (plain decoding, verify blocks) the
-// waves split the tokens (KW > 1), and long sequences are also split over
-// work-groups, whose partial sums a second kernel joins.
+// the head fastest, are cut into 32 per wave; a work-group of MW x KW waves
+// walks over the visible tokens in blocks of KW * KT, staged in LDS STAGES
+// deep, so that every wave reads each key and value once from there whatever
+// the page size and layout. Wave (mw, kw) takes the mw-th 32 rows and the
+// kw-th KT tokens of each block. With few query rows (plain decoding, verify
+// blocks) the waves split the tokens (KW > 1), and long sequences are also
+// split over work-groups, whose partial sums a second kernel joins. With many,
+// eight waves share a block's loads: two tiles of 128 rows, without a window
+// one from the chunk's beginning and one from its end, so that all work-groups
+// have as much to do.
+//
+// Loads go to LDS without registers between, up to STAGES - 1 blocks ahead. A
+// block's places in the cache are found before that: its entries of the page
+// table are asked for 2 STAGES - 1 blocks ahead (to LDS too: a wait for a
+// register would wait for all loads in flight), and turned into places STAGES
+// blocks ahead, each block by another wave.
 //
 // A wave forms S^T = K Q^T with 32x32x16 matrix instructions: lane l holds 16
 // scores of each 32 tokens for query row l % 32, so maxima and sums stay in
@@ -55,7 +64,7 @@ struct AttnArgs {
   unsigned page_units, slot_units, head_units;  // strides in 16-byte units
   float scale_log2;
   int window, sinks;
-  int tiles, split_blocks, splits;
+  int groups, split_blocks, splits;  // work-groups over a sequence's rows; of its tokens
   float* part;  // [n_rows * heads][splits][dim] sums, then [..][splits][2] (max, sum)
   float* part_ml;
 };
@@ -159,20 +168,27 @@ __device__ __forceinline__ int page_index(const AttnArgs& a, int t) {
   return a.page_mul ? (int)(__umulhi((unsigned)t, a.page_mul) >> a.page_shift) : t;
 }
 
-// 16 bytes per active lane from global memory to LDS at `lds` (uniform) + 16 *
-// lane, without registers between. It is an instruction of its own kind to the
-// compiler, which would otherwise wait for it before every LDS read: staged()
-// waits for it. The no-op covers the write of m0, which nothing
-// else here uses.
-__device__ __forceinline__ void load_to_lds(const void* from, unsigned lds) {
+// 16 (4) bytes per lane from global memory to LDS at `lds` (uniform) + 16 (4)
+// * lane, without registers between. These are no loads to the compiler, which
+// would wait for them before every LDS read: staged() waits for them. The
+// no-op covers the write of m0, which nothing else here uses.
+__device__ __forceinline__ void load16_to_lds(const void* from, unsigned lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                :
                : "s"(lds), "v"(from)
                : "memory");
 }
-// Everything this wave has asked for is there, and then every wave's.
+__device__ __forceinline__ void load4_to_lds(const void* from, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
+               :
+               : "s"(lds), "v"(from)
+               : "memory");
+}
+
+// All but the last FLIGHT loads of this wave are there, and then every wave's.
+template <int FLIGHT>
 __device__ __forceinline__ void staged() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(FLIGHT) : "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
@@ -191,15 +207,110 @@ __device__ __forceinline__ void pipelined() {
   __builtin_amdgcn_sched_group_barrier(0x008, ahead, 0);
 }
 
+// The order of STEPS runs of N matrix instructions on values, two LDS reads
+// each, and of the forming of weights: a run's 8 weights per lane (20 plain
+// and 8 transcendental instructions) go between the run's before.
+template <int STEPS, int N>
+__device__ __forceinline__ void interleaved() {
+  constexpr int ahead = 2;
+  __builtin_amdgcn_sched_group_barrier(0x002, 20, 0);
+  __builtin_amdgcn_sched_group_barrier(0x400, 8, 0);
+  __builtin_amdgcn_sched_group_barrier(0x100, 2 * ahead, 0);
+#pragma unroll
+  for (int i = 0; i < STEPS * N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (i + ahead < STEPS * N) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+    if (i / N + 1 < STEPS) {
+      constexpr int plain = (20 + N - 1) / N, trans = (8 + N - 1) / N;
+      __builtin_amdgcn_sched_group_barrier(0x400, trans, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, plain, 0);
+    }
+  }
+}
+
 // exp2((x - top) * scale), 0 where x is -inf (also when both are).
 __device__ __forceinline__ float exp_of(float x, float top, float scale) {
   return x == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((x - top) * scale);
+}
+
+// The lane's number, which the compiler cannot compute with ahead of a loop:
+// for code that seldom runs, so that what it needs does not take registers
+// from the loop.
+__device__ __forceinline__ int lane_here() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
 }
 
 __device__ __forceinline__ float max_of_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
                                                   false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ unsigned lds_offset(const void* p) {
+  return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// LDS addresses of a lane's share of the keys and values of a staged block, for
+// its first piece; the other pieces are a constant away, or an exclusive or
+// where the exchange of pieces reaches (stages begin at multiples of a row).
+template <int D>
+__device__ __forceinline__ unsigned key_address(int lane) {
+  const int row = lane & 31;
+  return row * D * 2 + k_piece<D / 8>(row, lane >> 5) * 16;
+}
+template <int D>
+__device__ __forceinline__ unsigned value_address(int lane) {
+  const int row = 4 * (lane >> 5) + (lane >> 2 & 3);
+  const int col = 16 * (lane >> 4 & 1) + 4 * (lane & 3);
+  return row * D * 2 + v_piece<D / 8>(row, col >> 3) * 16 + (col & 7) * 2;
+}
+
+// Keys of 32 tokens (u) and 16 columns (x), as the A operand.
+template <int D>
+__device__ __forceinline__ s16x8 keys(unsigned at, int u, int x) {
+  at = D / 8 % 8 == 0 ? (at ^ (x & 3) << 5) + (x >> 2) * 128 : at + x * 32;
+  return *(__attribute__((address_space(3))) s16x8*)(at + u * 32 * D * 2);
+}
+
+// Values of 16 tokens (u) and 32 columns (d), as the A operand: lane l of 16
+// reads 4 columns of token l / 4 and gets 4 tokens of column l % 16.
+template <int D>
+__device__ __forceinline__ s16x8 values(unsigned at, int u, int d) {
+  at = D / 8 % 16 == 0  ? (at ^ (d & 3) << 6) + (d >> 2) * 256
+       : D / 8 % 8 == 0 ? (at ^ (d & 1) << 6) + (d >> 1) * 128
+                        : at + d * 64;
+  s16x4 v[2];
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    v[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (__attribute__((address_space(3))) s16x4*)(at + (16 * u + 8 * y) * D * 2));
+  return __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// A block whose values hold infinities or NaN, some rows not seeing all of its
+// tokens. A function of its own: it seldom runs, and takes no registers from
+// the loop. `seen` are the bits of the tokens that the lane's row sees.
+template <int DB, int SUB>
+struct BadBlock {
+  f32x16 o[DB];
+  s16x8 weights[2 * SUB];
+};
+
+template <typename T, int D, int SUB>
+__device__ __attribute__((noinline)) void product_with_bad_values(
+    BadBlock<(D + 31) / 32, SUB>& x, unsigned seen, unsigned vs) {
+  vs += value_address<D>(threadIdx.x & 63);
+#pragma unroll
+  for (int d = 0; d < (D + 31) / 32; ++d) {
+    f32x16 o = x.o[d];
+    add_not_finite<T, 2 * SUB>([&](int u) { return values<D>(vs, u, d); }, seen, o);
+#pragma unroll
+    for (int u = 0; u < 2 * SUB; ++u)
+      o = mfma<T>(finite<T>(values<D>(vs, u, d)), x.weights[u], o);
+    x.o[d] = o;
+  }
 }
 
 // The tokens that the rows of a tile see, as blocks of BT tokens: `sink`
@@ -230,9 +341,29 @@ __device__ __forceinline__ int blocks_of_split(const AttnArgs& a, int all) {
   return max(a.split_blocks, (all + a.splits - 1) / a.splits);
 }
 
-template <typename T, int D, int MW, int KW, int KT>
+// The rows of a work-group: tiles `first` and `second` (the same where there
+// is no second), of `tiles` tiles of (row, head) pairs. PAIRS: two tiles.
+struct Tiles {
+  int first, second;
+};
+
+template <bool PAIRS>
+__device__ __forceinline__ Tiles tiles_of(int group, int tiles, bool window) {
+  if (!PAIRS) return Tiles{group, group};
+  if (window) return Tiles{2 * group, min(2 * group + 1, tiles - 1)};
+  return Tiles{group, tiles - 1 - group};
+}
+template <bool PAIRS>
+__device__ __forceinline__ int group_of(int tile, int tiles, bool window) {
+  if (!PAIRS) return tile;
+  return window ? tile / 2 : min(tile, tiles - 1 - tile);
+}
+
+template <typename T, int D, int MW, int KW, int KT, int STAGES>
 __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(const AttnArgs a) {
   constexpr int NW = MW * KW, BT = KW * KT, DC = D / 8, DS = D / 16, DB = (D + 31) / 32;
+  constexpr bool PAIRS = MW == 8;
+  constexpr int ROWS = PAIRS ? 128 : 32 * MW;        // (row, head) pairs of a tile
   constexpr int GROUPS = BT * DC / 64;               // of 64 pieces: a wave's access
   constexpr int LOADS = (GROUPS + NW - 1) / NW;      // per wave, of keys and of values
   constexpr int SUB = KT / 32;
@@ -240,47 +371,60 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
   // Where D is not a multiple of 32 the last column block of V reads past its
   // row, at the end past its stage (the results are not used).
   constexpr int VSTAGE = STAGE + (D % 32 ? 32 : 0);
-  __shared__ __align__(16) uint16_t lds[2 * (STAGE + VSTAGE)];
-  __shared__ unsigned places[4][BT];
-  __shared__ int holes;  // not 0: a page was missing
+  constexpr int RING = 8;                            // blocks whose places are held
+  static_assert(2 * STAGES - 1 <= RING && (STAGES & (STAGES - 1)) == 0, "");
+  __shared__ __align__(1024) uint16_t lds[STAGES * (STAGE + VSTAGE)];
+  __shared__ unsigned places[RING][BT];  // in the cache, in 16-byte units, or kNoPlace
+  __shared__ int entries[RING][BT];      // of the page table
+  __shared__ int holes;                  // not 0: a page was missing
 
   const int h = blockIdx.x % a.kv_heads;
   const int b = blockIdx.x / a.kv_heads % a.seqs.n_seqs;
   const int rest = blockIdx.x / a.kv_heads / a.seqs.n_seqs;
-  const int tile = a.tiles - 1 - rest % a.tiles;  // the longest first
-  const int split = rest / a.tiles;
+  const int group = a.groups - 1 - rest % a.groups;  // the longest first
+  const int split = rest / a.groups;
 
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mw = wave % MW, kw = wave / MW;
-  const int half = lane >> 5, ql = lane & 31;
 
   const int row0 = max(a.seqs.row_start[b], 0);
   const int n = min(min(a.seqs.row_start[b + 1], a.seqs.n_rows) - row0, a.seqs.max_rows);
-  const int g = a.group;
-  const int m0 = tile * MW * 32;
-  if (m0 >= n * g) return;
+  const int g = a.group, pairs = n * g;
+  const int tiles = (pairs + ROWS - 1) / ROWS;
+  if (n <= 0 || group >= (PAIRS ? (tiles + 1) / 2 : tiles)) return;
+  const Tiles tile = tiles_of<PAIRS>(group, tiles, a.window > 0);
   const int kv_len = a.seqs.kv_len[b];
   const int pos0 = kv_len - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
-  const int p0 = pos0 + m0 / g, p1 = pos0 + (min(m0 + MW * 32, n * g) - 1) / g;
-  const Blocks blocks = visible_blocks<BT>(p0, p1, kv_len, a.window, a.sinks);
+  const Blocks blocks =
+      visible_blocks<BT>(pos0 + tile.first * ROWS / g,
+                         pos0 + (min((tile.second + 1) * ROWS, pairs) - 1) / g, kv_len, a.window,
+                         a.sinks);
   const int per_split = blocks_of_split(a, blocks.all);
   const int parts = max((blocks.all + per_split - 1) / per_split, 1);
   if (split >= parts) return;
   const int j0 = split * per_split, j1 = min(j0 + per_split, blocks.all);
 
-  // This lane's query row, and its values as the B operand.
-  const int m = m0 + mw * 32 + ql;
-  const bool real = m < n * g;
-  const int qrow = real ? m / g : 0, qhead = h * g + (real ? m - qrow * g : 0);
-  const int pos = real ? pos0 + qrow : -1;
-  const int64_t qi = ((int64_t)(row0 + qrow) * (a.kv_heads * g) + qhead) * D;
+  // This wave's rows, and this lane's with its values as the B operand.
+  int m0 = (PAIRS ? mw < 4 ? tile.first : tile.second : tile.first) * ROWS + mw % (ROWS / 32) * 32;
+  if (PAIRS && mw >= 4 && tile.first == tile.second) m0 = pairs;  // none
+  const int p0 = pos0 + m0 / g, p1 = pos0 + (min(m0 + 32, pairs) - 1) / g;
+  struct Row {
+    bool real;
+    int64_t index;  // of (row, head), densely
+  };
+  const auto row_of = [&](int lane) {
+    const int m = m0 + (lane & 31), row = m / g;
+    return Row{m < pairs, (int64_t)(row0 + row) * (a.kv_heads * g) + h * g + m - row * g};
+  };
+  const Row mine = row_of(lane);
   s16x8 qf[DS];
 #pragma unroll
   for (int s = 0; s < DS; ++s) {
     qf[s] = s16x8{};
-    if (real)
-      qf[s] = *reinterpret_cast<const s16x8*>(static_cast<const uint16_t*>(a.q) + qi + 16 * s +
-                                              8 * half);
+    if (mine.real)
+      qf[s] = *reinterpret_cast<const s16x8*>(static_cast<const uint16_t*>(a.q) + mine.index * D +
+                                              16 * s + 8 * (lane >> 5));
   }
 
   f32x16 o[DB];
@@ -292,115 +436,122 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
     return (j < blocks.sink ? j : blocks.first + j - blocks.sink) * BT;
   };
 
-  // A block's tokens are looked up by as many threads, two blocks ahead of
-  // their loads (the entry of the table is asked for three ahead): places[]
-  // holds a token's place in the cache in 16-byte units, or kNoPlace.
   const char* kbase = static_cast<const char*>(a.k) + (uint64_t)h * a.head_units * 16;
   const char* vbase = static_cast<const char*>(a.v) + (uint64_t)h * a.head_units * 16;
   const int32_t* table = a.seqs.table + (int64_t)b * a.seqs.table_stride;
-  int entry = -1;
+  const auto place_of = [&](int t, int i, int entry) {
+    if (t < kv_len && i < a.seqs.table_width && (unsigned)entry < (unsigned)a.pages)
+      return (unsigned)entry * a.page_units + (unsigned)(t - i * a.page_size) * a.slot_units;
+    if (t < kv_len) holes = 1;
+    return kNoPlace;
+  };
+  // The wave whose turn block j is (or waves: 64 tokens each).
+  constexpr int TURN = (BT + 63) / 64;
+  const auto turn = [&](int j) { return (wave - (j - j0) * TURN) & (NW - 1); };
   const auto ask = [&](int j) {
-    entry = -1;
-    if ((int)threadIdx.x < BT && j < j1) {
-      const int t = base_of(j) + threadIdx.x, i = page_index(a, t);
-      if (t < kv_len && i < a.seqs.table_width) entry = table[i];
+    const int x = turn(j);
+    if (j < j1 && x < TURN && (BT % 64 == 0 || lane < BT)) {
+      const int i = min(page_index(a, base_of(j) + 64 * x + lane), a.seqs.table_width - 1);
+      load4_to_lds(table + i,
+                   __builtin_amdgcn_readfirstlane(lds_offset(&entries[(j - j0) % RING][64 * x])));
     }
   };
   const auto look_up = [&](int j) {
-    if ((int)threadIdx.x < BT && j < j1) {
-      const int t = base_of(j) + threadIdx.x;
-      unsigned place = kNoPlace;
-      if ((unsigned)entry < (unsigned)a.pages)
-        place = (unsigned)entry * a.page_units +
-                (unsigned)(t - page_index(a, t) * a.page_size) * a.slot_units;
-      else if (t < kv_len)
-        holes = 1;
-      places[(j - j0) & 3][threadIdx.x] = place;
+    const int x = turn(j);
+    if (j < j1 && x < TURN && (BT % 64 == 0 || lane < BT)) {
+      const int t = base_of(j) + 64 * x + lane;
+      places[(j - j0) % RING][64 * x + lane] =
+          place_of(t, page_index(a, t), entries[(j - j0) % RING][64 * x + lane]);
     }
   };
   // Piece p of a block's keys goes to LDS place p; it is piece k_piece(t, p %
-  // DC) of token t = p / DC, and likewise for the values. Values of tokens
-  // that are none are zeros, for the product; their scores are masked.
-  const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-  const auto load = [&](int j, int buf) {
-    const unsigned kl = lds0 + buf * (STAGE + VSTAGE) * 2, vl = kl + STAGE * 2;
-    uint16_t* vs = lds + buf * (STAGE + VSTAGE) + STAGE;
+  // DC) of token t = p / DC, and likewise for the values. A token that is none
+  // is loaded from the cache's first place and masked.
+  const auto load = [&](int j) {
+    const int buf = (j - j0) % STAGES;
+    const unsigned kl = lds_offset(lds) + buf * (STAGE + VSTAGE) * 2, vl = kl + STAGE * 2;
+    const int lane = lane_here();
     unsigned place[LOADS];
-    bool all = true;
 #pragma unroll
     for (int x = 0; x < LOADS; ++x) {
       const int g0 = x * NW + wave;
       if (GROUPS % NW && g0 >= GROUPS) continue;
-      place[x] = places[(j - j0) & 3][(g0 * 64 + lane) / DC];
-      all = all && place[x] != kNoPlace;
+      place[x] = places[(j - j0) % RING][(g0 * 64 + lane) / DC];
     }
-    const bool whole = __all(all);
 #pragma unroll
     for (int x = 0; x < LOADS; ++x) {
       const int g0 = x * NW + wave;
       if (GROUPS % NW && g0 >= GROUPS) continue;
       const int p = g0 * 64 + lane, t = p / DC, c = p % DC;
-      const unsigned kb = __builtin_amdgcn_readfirstlane(kl + g0 * 1024);
-      const unsigned vb = __builtin_amdgcn_readfirstlane(vl + g0 * 1024);
-      if (whole || place[x] != kNoPlace) {
-        load_to_lds(kbase + (uint64_t)(place[x] + k_piece<DC>(t, c)) * 16, kb);
-        load_to_lds(vbase + (uint64_t)(place[x] + v_piece<DC>(t, c)) * 16, vb);
-      } else {
-        *reinterpret_cast<u32x4*>(vs + p * 8) = u32x4{};
-      }
+      const unsigned at = place[x] == kNoPlace ? 0u : place[x];
+      load16_to_lds(kbase + (uint64_t)(at + k_piece<DC>(t, c)) * 16,
+                    __builtin_amdgcn_readfirstlane(kl + g0 * 1024));
+      load16_to_lds(vbase + (uint64_t)(at + v_piece<DC>(t, c)) * 16,
+                    __builtin_amdgcn_readfirstlane(vl + g0 * 1024));
     }
   };
 
+  // The waits for the query rows belong here, not in the loop behind loads.
+#pragma unroll
+  for (int x = 0; x < DS; ++x) asm volatile("" : "+v"(qf[x]));
   if (threadIdx.x == 0) holes = 0;
   __syncthreads();
-  ask(j0);
-  look_up(j0);
-  ask(j0 + 1);
-  look_up(j0 + 1);
-  __syncthreads();
-  if (j0 < j1) load(j0, 0);
-  ask(j0 + 2);
-  for (int j = j0; j < j1; ++j) {
-    const int buf = (j - j0) & 1;
-    // Block j is there for all, and all are done with the other buffer.
-    staged();
-    if (j + 1 < j1) {
-      asm volatile("" : "+v"(entry));  // the wait for it is over: not after the loads
-      load(j + 1, 1 - buf);
-      look_up(j + 2);
-      ask(j + 3);
+  for (int x = threadIdx.x; x < (2 * STAGES - 1) * BT; x += NW * 64) {
+    const int j = j0 + x / BT;
+    if (j < j1) {
+      const int t = base_of(j) + x % BT, i = page_index(a, t);
+      places[x / BT][x % BT] =
+          place_of(t, i, t < kv_len && i < a.seqs.table_width ? table[i] : -1);
     }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int x = 0; x < STAGES - 1; ++x)
+    if (j0 + x < j1) load(j0 + x);
+  for (int j = j0; j < j1; ++j) {
+    const int buf = (j - j0) % STAGES;
+    // Block j is there for all, and all are done with block j - 1.
+    if (STAGES > 2 && j + STAGES - 2 < j1)
+      staged<(STAGES - 2) * 2 * (GROUPS / NW)>();
+    else
+      staged<0>();
+    ask(j + 2 * STAGES - 1);
+    if (j + STAGES - 1 < j1) load(j + STAGES - 1);
+    if (j - j0 >= STAGES - 1) look_up(j + STAGES);
+
     const uint16_t* ks = lds + buf * (STAGE + VSTAGE) + kw * KT * D;
     const uint16_t* vs = lds + buf * (STAGE + VSTAGE) + STAGE + kw * KT * D;
     const int t0 = base_of(j) + kw * KT;
+    // Nothing to see for these rows.
+    if (t0 > p1 || m0 >= pairs ||
+        (a.window > 0 && t0 + KT <= p0 - a.window + 1 && t0 >= a.sinks))
+      continue;
 
     f32x16 s[SUB];
+    const unsigned ka = lds_offset(ks) + key_address<D>(lane);
+    const unsigned va = lds_offset(vs) + value_address<D>(lane);
 #pragma unroll
-    for (int x = 0; x < DS; ++x) {
+    for (int x = 0; x < DS; ++x)
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
-        const int row = 32 * u + ql;
-        const s16x8 kf = *reinterpret_cast<const s16x8*>(
-            ks + row * D + k_piece<DC>(row, 2 * x + half) * 8);
-        s[u] = mfma<T>(kf, qf[x], x ? s[u] : f32x16{});
-      }
-    }
+      for (int u = 0; u < SUB; ++u)
+        s[u] = mfma<T>(keys<D>(ka, u, x), qf[x], x ? s[u] : f32x16{});
     pipelined<SUB * DS, 1, 4>();
     // Hidden tokens, and those without a page. Where every row sees every token
     // there is nothing to mask.
     bool full = t0 + KT - 1 <= p0 && (a.window == 0 || t0 > p1 - a.window);
-    const bool whole = *const_cast<volatile int*>(&holes) == 0;
+    const bool whole = holes == 0;
     full = full && t0 + KT <= kv_len && whole;
     unsigned seen = 0;
     if (!full) {
       // Token t0 + 32 u + 8 (i / 4) + 4 half + i % 4, against the row's bounds.
-      const int hi = pos - t0 - 4 * half;
+      const int l = lane_here(), row = (m0 + (l & 31)) / g, half = l >> 5;
+      const int hi = (m0 + (l & 31) < pairs ? pos0 + row : -1) - t0 - 4 * half;
       const int lo = a.window > 0 ? hi - a.window : INT_MIN;
       const int sink = a.sinks - t0 - 4 * half;
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
         const unsigned paged =
-            (unsigned)__ballot(places[(j - j0) & 3][kw * KT + 32 * u + ql] != kNoPlace) >>
+            (unsigned)__ballot(places[(j - j0) % RING][kw * KT + 32 * u + (l & 31)] != kNoPlace) >>
             (4 * half);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -431,13 +582,22 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
         for (int i = 0; i < 16; ++i) o[d][i] *= back;
     }
     const float shift = mx == -__builtin_inff() ? 0.0f : mx * a.scale_log2;
+    // The weights of 16 tokens, as the B operand of their product.
+    const auto weights = [&](int u) {
+      u32x4 w;
 #pragma unroll
-    for (int u = 0; u < SUB; ++u)
+      for (int i = 0; i < 4; ++i) {
+        float p[2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        s[u][i] = __builtin_amdgcn_exp2f(fmaf(s[u][i], a.scale_log2, -shift));
-        sum += s[u][i];
+        for (int e = 0; e < 2; ++e) {
+          p[e] = __builtin_amdgcn_exp2f(
+              fmaf(s[u / 2][8 * (u & 1) + 2 * i + e], a.scale_log2, -shift));
+          sum += p[e];
+        }
+        w[i] = pack2<T>(p[0], p[1]);
       }
+      return __builtin_bit_cast(s16x8, w);
+    };
 
     // A hidden token's weight is 0, which an infinity or NaN of its values
     // would turn into NaN: where some rows do not see all tokens, such values
@@ -445,48 +605,33 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
     bool bad = false;
     if (!full) {
       unsigned found = 0;
-      for (int x = lane; x < KT * DC; x += 64) {
+      for (int x = lane_here(); x < KT * DC; x += 64) {
         const u32x4 w = *reinterpret_cast<const u32x4*>(vs + x * 8);
 #pragma unroll
         for (int e = 0; e < 4; ++e) found |= not_finite<T>(w[e]);
       }
       bad = __ballot(found != 0) != 0;
     }
-    const auto values = [&](int u, int d) {
-      // Lane l of 16 reads 4 columns of token l / 4; it gets 4 tokens of column l % 16.
-      s16x4 vf[2];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int row = 16 * u + 8 * y + 4 * half + (lane >> 2 & 3);
-        const int col = 32 * d + 16 * (lane >> 4 & 1) + 4 * (lane & 3);
-        const uint16_t* p = vs + row * D + v_piece<DC>(row, col >> 3) * 8 + (col & 7);
-        vf[y] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (__attribute__((address_space(3))) s16x4*)p);
-      }
-      return __builtin_shufflevector(vf[0], vf[1], 0, 1, 2, 3, 4, 5, 6, 7);
-    };
-    s16x8 pf[2 * SUB];
-#pragma unroll
-    for (int u = 0; u < 2 * SUB; ++u) {
-      u32x4 pw;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        pw[i] = pack2<T>(s[u / 2][8 * (u & 1) + 2 * i], s[u / 2][8 * (u & 1) + 2 * i + 1]);
-      pf[u] = __builtin_bit_cast(s16x8, pw);
-    }
     if (bad) {
+      BadBlock<DB, SUB> x;
 #pragma unroll
-      for (int d = 0; d < DB; ++d) {
-        add_not_finite<T, 2 * SUB>([&](int u) { return values(u, d); }, seen, o[d]);
+      for (int u = 0; u < 2 * SUB; ++u) x.weights[u] = weights(u);
 #pragma unroll
-        for (int u = 0; u < 2 * SUB; ++u) o[d] = mfma<T>(finite<T>(values(u, d)), pf[u], o[d]);
-      }
+      for (int d = 0; d < DB; ++d) x.o[d] = o[d];
+      product_with_bad_values<T, D, SUB>(x, seen, lds_offset(vs));
+#pragma unroll
+      for (int d = 0; d < DB; ++d) o[d] = x.o[d];
     } else {
+      // The next 16 tokens' weights are formed while the matrix unit works.
+      s16x8 next = weights(0);
 #pragma unroll
-      for (int u = 0; u < 2 * SUB; ++u)
+      for (int u = 0; u < 2 * SUB; ++u) {
+        const s16x8 pf = next;
 #pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] = mfma<T>(values(u, d), pf[u], o[d]);
-      pipelined<2 * SUB * DB, 2, 4>();
+        for (int d = 0; d < DB; ++d) o[d] = mfma<T>(values<D>(va, u, d), pf, o[d]);
+        if (u + 1 < 2 * SUB) next = weights(u + 1);
+      }
+      interleaved<2 * SUB, DB>();
     }
   }
   sum += __shfl_xor(sum, 32);
@@ -524,10 +669,12 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
     if (kw > 0) return;
   }
 
-  if (!real) return;
+  const int l = lane_here(), half = l >> 5;
+  const Row row = row_of(l);
+  if (!row.real) return;
   if (parts == 1) {
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + qi;
+    uint16_t* out = static_cast<uint16_t*>(a.out) + row.index * D;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -540,7 +687,7 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
         }
       }
   } else {
-    const int64_t at = ((int64_t)(row0 + qrow) * (a.kv_heads * g) + qhead) * a.splits + split;
+    const int64_t at = row.index * a.splits + split;
     float* out = a.part + at * D;
 #pragma unroll
     for (int d = 0; d < DB; ++d)
@@ -560,8 +707,8 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
 
 // Joins the partial sums of a (row, head): one work-group, 4 columns per
 // thread, so that 1024 / D (rounded down) parts are read at the same time.
-template <typename T, int D, int BT>
-__global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a, int rows_per_tile) {
+template <typename T, int D, int BT, int ROWS, bool PAIRS>
+__global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a) {
   constexpr int COLS = D / 4, SETS = 256 / COLS;
   __shared__ f32x4 sums[SETS][COLS];
   const int heads = a.kv_heads * a.group;
@@ -572,11 +719,15 @@ __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a, int row
   if (r < row0) return;
   const int n = min(min(a.seqs.row_start[b + 1], a.seqs.n_rows) - row0, a.seqs.max_rows);
   if (r - row0 >= n) return;
-  const int g = a.group, kv_len = a.seqs.kv_len[b];
+  const int g = a.group, kv_len = a.seqs.kv_len[b], tiles = (n * g + ROWS - 1) / ROWS;
   const int pos0 = kv_len - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
-  const int m0 = ((r - row0) * g + head % g) / rows_per_tile * rows_per_tile;
-  const int p0 = pos0 + m0 / g, p1 = pos0 + (min(m0 + rows_per_tile, n * g) - 1) / g;
-  const Blocks blocks = visible_blocks<BT>(p0, p1, kv_len, a.window, a.sinks);
+  const Tiles tile = tiles_of<PAIRS>(
+      group_of<PAIRS>(((r - row0) * g + head % g) / ROWS, tiles, a.window > 0), tiles,
+      a.window > 0);
+  const Blocks blocks =
+      visible_blocks<BT>(pos0 + tile.first * ROWS / g,
+                         pos0 + (min((tile.second + 1) * ROWS, n * g) - 1) / g, kv_len, a.window,
+                         a.sinks);
   const int per_split = blocks_of_split(a, blocks.all);
   const int parts = (blocks.all + per_split - 1) / per_split;
   if (parts <= 1) return;  // written by the first kernel
@@ -612,16 +763,16 @@ __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a, int row
   }
 }
 
-template <typename T, int D, int MW, int KW, int KT>
+template <typename T, int D, int MW, int KW, int KT, int STAGES>
 hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
-  const int64_t grid = (int64_t)a.kv_heads * a.seqs.n_seqs * a.tiles * a.splits;
-  hipLaunchKernelGGL((paged_attn<T, D, MW, KW, KT>), dim3((unsigned)grid), dim3(MW * KW * 64), 0,
-                     stream, a);
+  const int64_t grid = (int64_t)a.kv_heads * a.seqs.n_seqs * a.groups * a.splits;
+  hipLaunchKernelGGL((paged_attn<T, D, MW, KW, KT, STAGES>), dim3((unsigned)grid),
+                     dim3(MW * KW * 64), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((paged_attn_join<T, D, KW * KT>),
+  hipLaunchKernelGGL((paged_attn_join<T, D, KW * KT, MW == 8 ? 128 : 32 * MW, MW == 8>),
                      dim3((unsigned)(a.seqs.n_rows * a.kv_heads * a.group)), dim3(256), 0, stream,
-                     a, MW * 32);
+                     a);
   return hipGetLastError();
 }
 
@@ -632,9 +783,14 @@ constexpr int token_waves(int dim) { return dim <= 64 ? 4 : dim <= 128 ? 2 : 1; 
 template <typename T, int D>
 hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
   constexpr int kw = token_waves(D);
-  if (p.mw == 4) return launch_shape<T, D, 4, 1, D <= 128 ? 64 : 32>(a, stream);
-  if (p.mw == 2) return launch_shape<T, D, 2, kw < 2 ? kw : 2, 32>(a, stream);
-  return launch_shape<T, D, 1, kw, 32>(a, stream);
+  if constexpr (D <= 128) {
+    if (p.mw == 8) return launch_shape<T, D, 8, 1, 64, 4>(a, stream);
+    if (p.mw == 4) return launch_shape<T, D, 4, 1, 64, 2>(a, stream);
+  } else {
+    if (p.mw == 4) return launch_shape<T, D, 4, 1, 32, 4>(a, stream);
+  }
+  if (p.mw == 2) return launch_shape<T, D, 2, kw < 2 ? kw : 2, 32, 2>(a, stream);
+  return launch_shape<T, D, 1, kw, 32, 2>(a, stream);
 }
 
 template <typename T>
@@ -661,10 +817,10 @@ AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window,
   const int64_t m = (int64_t)(s.max_rows < s.n_rows ? s.max_rows : s.n_rows) * (heads / c.kv_heads);
   const int kw = token_waves(c.dim);
   AttnPlan p;
-  p.mw = m <= 32 ? 1 : m <= 64 ? 2 : 4;
-  p.kw = p.mw == 4 ? 1 : p.mw == 2 && kw > 2 ? 2 : kw;
-  p.kt = p.mw == 4 && c.dim <= 128 ? 64 : 32;
-  p.tiles = ceil_div(m < 1 ? 1 : m, 32 * p.mw);
+  p.mw = m <= 32 ? 1 : m <= 64 ? 2 : m <= 128 || c.dim > 128 ? 4 : 8;
+  p.kw = p.mw >= 4 ? 1 : p.mw == 2 && kw > 2 ? 2 : kw;
+  p.kt = p.mw >= 4 && c.dim <= 128 ? 64 : 32;
+  p.groups = ceil_div(m < 1 ? 1 : m, 32 * p.mw);
   const int bt = p.kw * p.kt;
   // The most blocks that a tile's rows see.
   int64_t tokens = s.max_kv;
@@ -675,17 +831,17 @@ AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window,
     tokens = seen < tokens ? seen : tokens;
   }
   const int blocks = ceil_div(tokens < 1 ? 1 : tokens, bt);
-  const int64_t base = (int64_t)c.kv_heads * s.n_seqs * p.tiles;
-  // Blocks of a split. Full tiles: two work-groups for each of the 256 CUs in
-  // one round, splits of 4 blocks at least. Few query rows: one work-group per
+  const int64_t base = (int64_t)c.kv_heads * s.n_seqs * p.groups;
+  // Blocks of a split. Full tiles: as many work-groups as fit the 256 CUs at
+  // once, splits of 4 blocks at least. Few query rows: one work-group per
   // CU while that leaves splits of 16 blocks or fewer (a block of 8 rows over
   // 4096 tokens: 14.6 us, with two per CU 16.3, one for two CUs 16.7); then
   // splits of 16 or more, in 16 rounds as lengths differ (48 ragged sequences:
   // 376 us, in 8 rounds 403, in 4 455), but in two where a window makes them
   // alike (74 us, in 4 rounds 82).
   int64_t per;
-  if (p.mw == 4) {
-    per = ceil_div(blocks * base, 512);
+  if (p.mw >= 4) {
+    per = ceil_div(blocks * base, p.mw == 4 && c.dim <= 128 ? 512 : 256);
     if (per < 4) per = 4;
   } else {
     per = ceil_div(blocks * base, 256);
@@ -731,7 +887,7 @@ hipError_t launch_paged_attn(const void* q, const vqv_cache& c, int layer, const
   a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
-  a.tiles = plan.tiles;
+  a.groups = plan.groups;
   a.split_blocks = plan.split_blocks;
   a.splits = plan.splits;
   a.part = static_cast<float*>(workspace);

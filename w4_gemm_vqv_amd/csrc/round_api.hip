@@ -208,7 +208,7 @@ vqv_status plan_attn(const vqv_cache* cache, const vqv_seqs* seqs, int heads, in
       (int64_t)seqs->n_rows * heads >= (1ll << 26))
     return VQV_ERR_UNSUPPORTED;
   *plan = vqv::attn_plan(*cache, *seqs, heads, window, sinks);
-  if ((int64_t)cache->kv_heads * seqs->n_seqs * plan->tiles * plan->splits >= (1ll << 23))
+  if ((int64_t)cache->kv_heads * seqs->n_seqs * plan->groups * plan->splits >= (1ll << 23))
     return VQV_ERR_UNSUPPORTED;
   return VQV_OK;
 }

@@ -21,12 +21,12 @@ hipError_t launch_rope_append(const RowsIn& q, const RowsIn& k, const RowsIn& v,
                               int heads, const vqv_cache& cache, int layer, const vqv_seqs& seqs,
                               const vqv_rope& rope, void* q_out, hipStream_t stream);
 
-// How an attention call is cut (attn.hip): the query rows of a tile, the
+// How an attention call is cut (attn.hip): the query rows of a work-group, the
 // blocks of tokens of a split, and the splits that the longest sequence has
 // (1: no partials and no second kernel).
 struct AttnPlan {
   int mw, kw, kt;      // waves over query rows, over tokens; tokens per wave
-  int tiles;           // tiles of 32 * mw (row, head) pairs per sequence and key head
+  int groups;          // of 32 * mw (row, head) pairs per sequence and key head
   int split_blocks;    // blocks of kw * kt tokens per split
   int splits;
 };
