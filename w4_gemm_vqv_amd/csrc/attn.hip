@@ -8,9 +8,11 @@
 // kw-th KT tokens of each block. With few query rows (plain decoding, verify
 // blocks) the waves split the tokens (KW > 1), and long sequences are also
 // split over work-groups, whose partial sums a second kernel joins. With many,
-// eight waves share a block's loads: two tiles of 128 rows, without a window
-// one from the chunk's beginning and one from its end, so that all work-groups
-// have as much to do.
+// eight waves share a block's loads: two tiles of 128 rows, one from the
+// chunk's beginning and one from its end, so that all work-groups have as much
+// to do (2048 rows of 32 heads over 10240 tokens: 379 us, with one tile per
+// work-group 405). Under a window the two would not see the same tokens: one
+// tile (3 chunks of up to 1500 rows, window 1023: 73 us, with two 78).
 //
 // Loads go to LDS without registers between, up to STAGES - 1 blocks ahead. A
 // block's places in the cache are found before that: its entries of the page
@@ -193,39 +195,19 @@ __device__ __forceinline__ void staged() {
   asm volatile("" ::: "memory");
 }
 
-// The order of a run of N matrix instructions that each take READS LDS reads:
-// the reads of AHEAD of them go first, and then one's with each.
-template <int N, int READS, int AHEAD>
+// The order of a run of N matrix instructions that each take an LDS read: the
+// reads of AHEAD of them go first, and then one's with each (left to itself the
+// compiler waits for each read in turn: a prompt chunk took 709 us, not 439).
+template <int N, int AHEAD>
 __device__ __forceinline__ void pipelined() {
   constexpr int ahead = N < AHEAD ? N : AHEAD;
-  __builtin_amdgcn_sched_group_barrier(0x100, READS * ahead, 0);
+  __builtin_amdgcn_sched_group_barrier(0x100, ahead, 0);
 #pragma unroll
   for (int i = 0; i < N - ahead; ++i) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
   }
   __builtin_amdgcn_sched_group_barrier(0x008, ahead, 0);
-}
-
-// The order of STEPS runs of N matrix instructions on values, two LDS reads
-// each, and of the forming of weights: a run's 8 weights per lane (20 plain
-// and 8 transcendental instructions) go between the run's before.
-template <int STEPS, int N>
-__device__ __forceinline__ void interleaved() {
-  constexpr int ahead = 2;
-  __builtin_amdgcn_sched_group_barrier(0x002, 20, 0);
-  __builtin_amdgcn_sched_group_barrier(0x400, 8, 0);
-  __builtin_amdgcn_sched_group_barrier(0x100, 2 * ahead, 0);
-#pragma unroll
-  for (int i = 0; i < STEPS * N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (i + ahead < STEPS * N) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-    if (i / N + 1 < STEPS) {
-      constexpr int plain = (20 + N - 1) / N, trans = (8 + N - 1) / N;
-      __builtin_amdgcn_sched_group_barrier(0x400, trans, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, plain, 0);
-    }
-  }
 }
 
 // exp2((x - top) * scale), 0 where x is -inf (also when both are).
@@ -342,21 +324,19 @@ __device__ __forceinline__ int blocks_of_split(const AttnArgs& a, int all) {
 }
 
 // The rows of a work-group: tiles `first` and `second` (the same where there
-// is no second), of `tiles` tiles of (row, head) pairs. PAIRS: two tiles.
+// is no second), of `tiles` tiles of (row, head) pairs. PAIRS: two tiles, as
+// far from the chunk's middle.
 struct Tiles {
   int first, second;
 };
 
 template <bool PAIRS>
-__device__ __forceinline__ Tiles tiles_of(int group, int tiles, bool window) {
-  if (!PAIRS) return Tiles{group, group};
-  if (window) return Tiles{2 * group, min(2 * group + 1, tiles - 1)};
-  return Tiles{group, tiles - 1 - group};
+__device__ __forceinline__ Tiles tiles_of(int group, int tiles) {
+  return Tiles{group, PAIRS ? tiles - 1 - group : group};
 }
 template <bool PAIRS>
-__device__ __forceinline__ int group_of(int tile, int tiles, bool window) {
-  if (!PAIRS) return tile;
-  return window ? tile / 2 : min(tile, tiles - 1 - tile);
+__device__ __forceinline__ int group_of(int tile, int tiles) {
+  return PAIRS ? min(tile, tiles - 1 - tile) : tile;
 }
 
 template <typename T, int D, int MW, int KW, int KT, int STAGES>
@@ -393,7 +373,7 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
   const int g = a.group, pairs = n * g;
   const int tiles = (pairs + ROWS - 1) / ROWS;
   if (n <= 0 || group >= (PAIRS ? (tiles + 1) / 2 : tiles)) return;
-  const Tiles tile = tiles_of<PAIRS>(group, tiles, a.window > 0);
+  const Tiles tile = tiles_of<PAIRS>(group, tiles);
   const int kv_len = a.seqs.kv_len[b];
   const int pos0 = kv_len - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
   const Blocks blocks =
@@ -535,7 +515,7 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
 #pragma unroll
       for (int u = 0; u < SUB; ++u)
         s[u] = mfma<T>(keys<D>(ka, u, x), qf[x], x ? s[u] : f32x16{});
-    pipelined<SUB * DS, 1, 4>();
+    pipelined<SUB * DS, 4>();
     // Hidden tokens, and those without a page. Where every row sees every token
     // there is nothing to mask.
     bool full = t0 + KT - 1 <= p0 && (a.window == 0 || t0 > p1 - a.window);
@@ -631,7 +611,6 @@ __global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(con
         for (int d = 0; d < DB; ++d) o[d] = mfma<T>(values<D>(va, u, d), pf, o[d]);
         if (u + 1 < 2 * SUB) next = weights(u + 1);
       }
-      interleaved<2 * SUB, DB>();
     }
   }
   sum += __shfl_xor(sum, 32);
@@ -721,9 +700,8 @@ __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a) {
   if (r - row0 >= n) return;
   const int g = a.group, kv_len = a.seqs.kv_len[b], tiles = (n * g + ROWS - 1) / ROWS;
   const int pos0 = kv_len - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
-  const Tiles tile = tiles_of<PAIRS>(
-      group_of<PAIRS>(((r - row0) * g + head % g) / ROWS, tiles, a.window > 0), tiles,
-      a.window > 0);
+  const Tiles tile =
+      tiles_of<PAIRS>(group_of<PAIRS>(((r - row0) * g + head % g) / ROWS, tiles), tiles);
   const Blocks blocks =
       visible_blocks<BT>(pos0 + tile.first * ROWS / g,
                          pos0 + (min((tile.second + 1) * ROWS, n * g) - 1) / g, kv_len, a.window,
@@ -817,7 +795,7 @@ AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window,
   const int64_t m = (int64_t)(s.max_rows < s.n_rows ? s.max_rows : s.n_rows) * (heads / c.kv_heads);
   const int kw = token_waves(c.dim);
   AttnPlan p;
-  p.mw = m <= 32 ? 1 : m <= 64 ? 2 : m <= 128 || c.dim > 128 ? 4 : 8;
+  p.mw = m <= 32 ? 1 : m <= 64 ? 2 : m <= 128 || c.dim > 128 || window > 0 ? 4 : 8;
   p.kw = p.mw >= 4 ? 1 : p.mw == 2 && kw > 2 ? 2 : kw;
   p.kt = p.mw >= 4 && c.dim <= 128 ? 64 : 32;
   p.groups = ceil_div(m < 1 ? 1 : m, 32 * p.mw);

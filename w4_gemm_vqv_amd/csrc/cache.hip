@@ -63,25 +63,29 @@ __device__ unsigned free_bits(const int32_t* __restrict__ ref, int pages, int p0
   return m;
 }
 
-// How many pages are free, counted only until `enough`.
-__device__ int count_free(const int32_t* __restrict__ ref, int pages, int enough, int* waves) {
+// How many pages are free, counted only until `enough`. `first` are the free
+// bits of this thread's pages of the first step.
+__device__ int count_free(const int32_t* __restrict__ ref, int pages, int enough, unsigned first,
+                          int* waves) {
   int found = 0;
   for (int base = 0; base < pages && found < enough; base += kStep) {
+    const unsigned m = base ? free_bits(ref, pages, base + threadIdx.x * kPer) : first;
     int all;
-    scan_block(__popc(free_bits(ref, pages, base + threadIdx.x * kPer)), waves, &all);
+    scan_block(__popc(m), waves, &all);
     found += all;
   }
   return found;
 }
 
 // Calls give(rank, page) for the `want` lowest free pages, and marks them
-// with one reference. off[] (n entries, ascending) is left to `give`.
+// with one reference.
 template <typename F>
-__device__ void give_free(int32_t* __restrict__ ref, int pages, int want, int* waves, F give) {
+__device__ void give_free(int32_t* __restrict__ ref, int pages, int want, unsigned first,
+                          int* waves, F give) {
   int found = 0;
   for (int base = 0; base < pages && found < want; base += kStep) {
     const int p0 = base + threadIdx.x * kPer;
-    unsigned m = free_bits(ref, pages, p0);
+    unsigned m = base ? free_bits(ref, pages, p0) : first;
     const int mine = __popc(m);
     int all;
     int rank = found + scan_block(mine, waves, &all) - mine;
@@ -137,21 +141,28 @@ __global__ __launch_bounds__(64) void cache_trim(const vqv_pages pg,
   }
 }
 
-// One work-group. off[]: the rank of each row's first new page.
+// One work-group. off[]: the rank of each row's first new page, in LDS while
+// the rows fit there. Loads that do not depend on each other go out together,
+// and what a thread has read it keeps, as their latency is all the time there
+// is (32 rows and 6000 pages: see the end of a round).
 __global__ __launch_bounds__(kBook) void cache_reserve(const vqv_pages pg,
                                                        const int32_t* __restrict__ goal_len,
                                                        int n, int32_t* __restrict__ ok,
-                                                       int32_t* __restrict__ off) {
+                                                       int32_t* __restrict__ scratch) {
   __shared__ int waves[kBook / 64];
+  __shared__ int held_of[kBook], off_of[kBook];
   __shared__ int granted;
+  const bool few = n <= kBook;
+  int32_t* off = few ? off_of : scratch;
+  const unsigned first = free_bits(pg.ref, pg.pages, threadIdx.x * kPer);
   if (threadIdx.x == 0) granted = 0;
-  int total = 0;
+  int total = 0, goal = 0, held = 0, need = 0;
   for (int base = 0; base < n; base += kBook) {
     const int i = base + threadIdx.x;
-    int need = 0;
+    need = 0;
     if (i < n) {
-      const int goal = pages_for(goal_len[i], pg.page_size);
-      const int held = clamp_int(pg.held[i], 0, pg.width);
+      goal = pages_for(goal_len[i], pg.page_size);
+      held = clamp_int(pg.held[i], 0, pg.width);
       need = goal <= pg.width ? max(goal - held, 0) : 0;
     }
     int all;
@@ -159,26 +170,29 @@ __global__ __launch_bounds__(kBook) void cache_reserve(const vqv_pages pg,
     if (i < n) off[i] = total + end - need;
     total = min(total + all, INT_MAX / 2);
   }
-  const int found = total ? count_free(pg.ref, pg.pages, total, waves) : 0;
+  held_of[threadIdx.x] = held;  // of the only step where the rows are few
+  const int found = total ? count_free(pg.ref, pg.pages, total, first, waves) : 0;
   for (int i = threadIdx.x; i < n; i += kBook) {
-    const int goal = pages_for(goal_len[i], pg.page_size);
-    const int held = clamp_int(pg.held[i], 0, pg.width);
-    const int need = goal <= pg.width ? max(goal - held, 0) : 0;
+    if (!few) {
+      goal = pages_for(goal_len[i], pg.page_size);
+      held = clamp_int(pg.held[i], 0, pg.width);
+      need = goal <= pg.width ? max(goal - held, 0) : 0;
+    }
     const bool good = goal <= pg.width && (need == 0 || off[i] + need <= found);
     ok[i] = good;
     if (good && need) atomicMax(&granted, off[i] + need);
   }
   __syncthreads();
   const int want = granted;
-  give_free(pg.ref, pg.pages, want, waves, [&](int rank, int p) {
+  give_free(pg.ref, pg.pages, want, first, waves, [&](int rank, int p) {
     const int i = owner_of(off, n, rank);
-    const int held = clamp_int(pg.held[i], 0, pg.width);
-    pg.table[(int64_t)i * pg.width + held + rank - off[i]] = p;
+    const int h = few ? held_of[i] : clamp_int(pg.held[i], 0, pg.width);
+    pg.table[(int64_t)i * pg.width + h + rank - off[i]] = p;
   });
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kBook)
     if (ok[i]) {
-      const int goal = pages_for(goal_len[i], pg.page_size);
+      if (!few) goal = pages_for(goal_len[i], pg.page_size);
       if (goal > pg.held[i]) pg.held[i] = goal;
     }
 }
@@ -228,9 +242,10 @@ __global__ __launch_bounds__(kBook) void cache_fork_book(
     if (i < n) off[i] = total + end - need;
     total += all;
   }
-  const int found = total ? min(count_free(pg.ref, pg.pages, total, waves), total) : 0;
+  const unsigned first = free_bits(pg.ref, pg.pages, threadIdx.x * kPer);
+  const int found = total ? min(count_free(pg.ref, pg.pages, total, first, waves), total) : 0;
   __syncthreads();
-  give_free(pg.ref, pg.pages, found, waves, [&](int rank, int p) {
+  give_free(pg.ref, pg.pages, found, first, waves, [&](int rank, int p) {
     to[owner_of(off, n, rank)] = p;
   });
   for (int i = threadIdx.x; i < n; i += kBook)
