@@ -340,7 +340,8 @@ __device__ __forceinline__ int group_of(int tile, int tiles) {
 }
 
 template <typename T, int D, int MW, int KW, int KT, int STAGES>
-__global__ __launch_bounds__(MW * KW * 64, D <= 128 ? 2 : 1) void paged_attn(const AttnArgs a) {
+__global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void paged_attn(
+    const AttnArgs a) {
   constexpr int NW = MW * KW, BT = KW * KT, DC = D / 8, DS = D / 16, DB = (D + 31) / 32;
   constexpr bool PAIRS = MW == 8;
   constexpr int ROWS = PAIRS ? 128 : 32 * MW;        // (row, head) pairs of a tile
