@@ -197,13 +197,17 @@ __global__ __launch_bounds__(kBook) void cache_reserve(const vqv_pages pg,
     }
 }
 
-// The book of a fork, one work-group: which pairs are good, their new pages,
-// the children's tables; from[i] and to[i] are the pages to copy, or -1.
+// The book of a fork, one work-group: which pairs are good, and their new
+// pages; from[i] and to[i] are the pages to copy, or -1. The children's tables
+// are written next to the copies, where the whole GPU is at hand.
 __global__ __launch_bounds__(kBook) void cache_fork_book(
     const vqv_pages pg, const int32_t* __restrict__ parent, const int32_t* __restrict__ child,
     int n, int32_t* __restrict__ ok, int32_t* __restrict__ named, int32_t* __restrict__ parents,
-    int32_t* __restrict__ off, int32_t* __restrict__ from, int32_t* __restrict__ to) {
+    int32_t* __restrict__ scratch, int32_t* __restrict__ from, int32_t* __restrict__ to) {
   __shared__ int waves[kBook / 64];
+  __shared__ int off_of[kBook];
+  int32_t* off = n <= kBook ? off_of : scratch;
+  const unsigned first = free_bits(pg.ref, pg.pages, threadIdx.x * kPer);
   for (int i = threadIdx.x; i < pg.rows; i += kBook) {
     named[i] = INT_MAX;
     parents[i] = 0;
@@ -242,7 +246,6 @@ __global__ __launch_bounds__(kBook) void cache_fork_book(
     if (i < n) off[i] = total + end - need;
     total += all;
   }
-  const unsigned first = free_bits(pg.ref, pg.pages, threadIdx.x * kPer);
   const int found = total ? min(count_free(pg.ref, pg.pages, total, first, waves), total) : 0;
   __syncthreads();
   give_free(pg.ref, pg.pages, found, first, waves, [&](int rank, int p) {
@@ -253,27 +256,36 @@ __global__ __launch_bounds__(kBook) void cache_fork_book(
       ok[i] = 0;
       to[i] = -1;
     }
-  __syncthreads();
-  const int lane = threadIdx.x & 63;
-  for (int i = threadIdx.x >> 6; i < n; i += kBook / 64) {
-    if (!ok[i]) continue;
-    const int p = parent[i], c = child[i];
-    const int held = clamp_int(pg.held[p], 0, pg.width);
-    const int length = max(pg.length[p], 0);
-    const int full = min(length / pg.page_size, held);
-    const int32_t* tp = pg.table + (int64_t)p * pg.width;
-    int32_t* tc = pg.table + (int64_t)c * pg.width;
-    for (int j = lane; j < full; j += 64) {
-      const int page = tp[j];
-      tc[j] = page;
-      if ((unsigned)page < (unsigned)pg.pages) atomicAdd(&pg.ref[page], 1);
-    }
-    if (lane == 0) {
-      const int own = to[i] >= 0;
-      if (own) tc[full] = to[i];
-      pg.held[c] = full + own;
-      pg.length[c] = own ? length : full * pg.page_size;
-    }
+}
+
+// What a fork's copies write of its book.
+struct Branches {
+  vqv_pages pages;
+  const int32_t* parent;
+  const int32_t* child;
+  const int32_t* ok;
+};
+
+// The table, held and length of branch i (new page `own`, or -1), by a
+// work-group of 256. Parents are no children, so nothing read here changes.
+__device__ __forceinline__ void write_branch(const Branches& f, int i, int own) {
+  const vqv_pages& pg = f.pages;
+  if (!f.ok[i]) return;
+  const int p = f.parent[i], c = f.child[i];
+  const int held = clamp_int(pg.held[p], 0, pg.width);
+  const int length = max(pg.length[p], 0);
+  const int full = min(length / pg.page_size, held);
+  const int32_t* tp = pg.table + (int64_t)p * pg.width;
+  int32_t* tc = pg.table + (int64_t)c * pg.width;
+  for (int j = threadIdx.x; j < full; j += 256) {
+    const int page = tp[j];
+    tc[j] = page;
+    if ((unsigned)page < (unsigned)pg.pages) atomicAdd(&pg.ref[page], 1);
+  }
+  if (threadIdx.x == 0) {
+    if (own >= 0) tc[full] = own;
+    pg.held[c] = full + (own >= 0);
+    pg.length[c] = own >= 0 ? length : full * pg.page_size;
   }
 }
 
@@ -289,17 +301,19 @@ struct PageShape {
 typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
 
 // One work-group per kCopy pieces of a page, layer and tensor. DENSE: a page
-// is one run of bytes.
+// is one run of bytes. FORK: the first work-group of a pair writes the branch.
 constexpr int kCopyPer = 4;
 constexpr int kCopy = 256 * kCopyPer;
 
-template <bool DENSE>
+template <bool DENSE, bool FORK>
 __global__ __launch_bounds__(256) void cache_copy(uint16_t* __restrict__ k,
                                                   uint16_t* __restrict__ v, const PageShape s,
                                                   const int32_t* __restrict__ src,
-                                                  const int32_t* __restrict__ dst) {
+                                                  const int32_t* __restrict__ dst,
+                                                  const Branches f) {
   const int i = blockIdx.y;
   const int from = src[i], to = dst[i];
+  if (FORK && blockIdx.x == 0 && blockIdx.z == 0) write_branch(f, i, to);
   if ((unsigned)from >= (unsigned)s.pages || (unsigned)to >= (unsigned)s.pages || from == to)
     return;
   uint16_t* base = (blockIdx.z & 1 ? v : k) + (int64_t)(blockIdx.z >> 1) * s.layer_stride;
@@ -394,8 +408,9 @@ __global__ __launch_bounds__(256) void cache_compact(const vqv_cache c, const vq
   if (blockIdx.x == 0 && threadIdx.x == 0) new_len[b] = p0 + done;
 }
 
+template <bool FORK>
 hipError_t launch_copy(const vqv_cache& c, const int32_t* src, const int32_t* dst, int n,
-                       hipStream_t stream) {
+                       Branches f, hipStream_t stream) {
   PageShape s{};
   s.layer_stride = c.layer_stride;
   s.page_stride = c.page_stride;
@@ -413,14 +428,14 @@ hipError_t launch_copy(const vqv_cache& c, const int32_t* src, const int32_t* ds
   // The grid's y holds 65535 pairs at a time.
   for (int i = 0; i < n; i += 65535) {
     const dim3 grid((s.pieces + kCopy - 1) / kCopy, n - i < 65535 ? n - i : 65535, c.layers * 2);
-    if (dense)
-      hipLaunchKernelGGL(cache_copy<true>, grid, dim3(256), 0, stream,
-                         static_cast<uint16_t*>(c.k), static_cast<uint16_t*>(c.v), s, src + i,
-                         dst + i);
-    else
-      hipLaunchKernelGGL(cache_copy<false>, grid, dim3(256), 0, stream,
-                         static_cast<uint16_t*>(c.k), static_cast<uint16_t*>(c.v), s, src + i,
-                         dst + i);
+    const auto kernel = dense ? cache_copy<true, FORK> : cache_copy<false, FORK>;
+    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, static_cast<uint16_t*>(c.k),
+                       static_cast<uint16_t*>(c.v), s, src + i, dst + i, f);
+    if (FORK) {
+      f.parent += 65535;
+      f.child += 65535;
+      f.ok += 65535;
+    }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -431,7 +446,7 @@ hipError_t launch_copy(const vqv_cache& c, const int32_t* src, const int32_t* ds
 
 hipError_t launch_cache_copy(const vqv_cache& cache, const int32_t* src, const int32_t* dst,
                              int n, hipStream_t stream) {
-  return launch_copy(cache, src, dst, n, stream);
+  return launch_copy<false>(cache, src, dst, n, Branches{}, stream);
 }
 
 hipError_t launch_cache_trim(const vqv_pages& pages, const int32_t* keep_len, const int32_t* rows,
@@ -457,7 +472,7 @@ hipError_t launch_cache_fork(const vqv_cache& cache, const vqv_pages& pages,
                      ok, named, parents, off, from, to);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return launch_copy(cache, from, to, n, stream);
+  return launch_copy<true>(cache, from, to, n, Branches{pages, parent, child, ok}, stream);
 }
 
 hipError_t launch_cache_compact(const vqv_cache& cache, const vqv_seqs& seqs, const int32_t* keep,
