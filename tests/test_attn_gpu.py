@@ -160,6 +160,23 @@ def test_past_the_table_and_lengths(vqv):
     assert (got[3:5] == 0).all() and (got[8:] == 0).all()
 
 
+@pytest.mark.parametrize("ps", [1, 16])
+@pytest.mark.parametrize("rows", [2, 150])
+def test_lengths_past_any_table(vqv, rows, ps):
+    """A kv_len near 2^31: the tokens that the table holds are seen by all rows."""
+    gen = torch.Generator().manual_seed(3)
+    n = 64 // ps
+    k, v = (torch.randn(1, n, ps, 1, 64, generator=gen).to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(rows, 2, 64, generator=gen).to(torch.bfloat16)
+    seqs = vqv.Sequences(i32([0, rows]), i32([2 ** 31 - 1]), i32([list(range(n))]), n_rows=rows,
+                         max_rows=rows, max_kv=64)
+    got = vqv.vqv_paged_attn(q.cuda(), vqv.PagedCache(k.cuda(), v.cuda()), seqs, scale=0.125).cpu()
+    c = Case(rows=[1], kv=[64], heads=2, hk=1, dim=64, ps=ps)
+    # as single rows at the end of 64 tokens
+    want = ref.attn_ref(q, k[0], v[0], list(range(rows + 1)), [64] * rows, [list(range(n))] * rows, 0.125)
+    c.close(got, want)
+
+
 def test_longer_than_planned(vqv):
     """A max_kv below the real lengths costs speed, not results."""
     for rows in ([2, 1], [80, 3]):

@@ -151,6 +151,13 @@ def test_attn_refusals(R, L, kw, status):
     assert attn_call(R, L, **kw) == status
 
 
+def test_attn_grid_limits(R, L):
+    """More work-groups than a launch can count."""
+    assert attn_call(R, L, s=seqs(R, n_rows=1 << 20, max_rows=1 << 20), heads=1024,
+                     wn=1 << 60) == UNSUP
+    assert attn_call(R, L, s=seqs(R, n_rows=1 << 20, n_seqs=1), heads=32, wn=1 << 60) == UNSUP
+
+
 def test_attn_dims(R, L):
     for d in (8, 72, 136, 248):
         assert attn_call(R, L, c=cache(R, dim=d)) == UNSUP

@@ -304,9 +304,9 @@ struct Blocks {
 template <int BT>
 __device__ __forceinline__ Blocks visible_blocks(int p0, int p1, int kv_len, int window,
                                                  int sinks) {
-  const int hi = min(p1 + 1, kv_len);
+  const int hi = p1 < kv_len ? p1 + 1 : kv_len;
   if (hi <= 0) return Blocks{0, 0, 0};
-  const int lo = window > 0 ? max(p0 - window + 1, 0) : 0;
+  const int lo = window > 0 ? min(max(p0 - window + 1, 0), hi) : 0;
   const int sink_end = min(sinks, lo);
   Blocks r;
   r.sink = window > 0 && sink_end > 0 ? (sink_end + BT - 1) / BT : 0;
@@ -315,6 +315,13 @@ __device__ __forceinline__ Blocks visible_blocks(int p0, int p1, int kv_len, int
   r.first = max(lo / BT, r.sink);
   r.all = r.sink + max(last - r.first, 0);
   return r;
+}
+
+// Tokens of a sequence that a table can hold; those past it are hidden. Places
+// in blocks are counted in 32 bits, with room for a block more.
+__device__ __forceinline__ int tokens_of(const AttnArgs& a, int kv_len) {
+  const int64_t room = (int64_t)a.seqs.table_width * a.page_size;
+  return (int)min((int64_t)kv_len, min(room, (int64_t)1 << 30));
 }
 
 // Blocks of a split: the plan's, or more where a sequence is longer than the
@@ -375,8 +382,8 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
   const int tiles = (pairs + ROWS - 1) / ROWS;
   if (n <= 0 || group >= (PAIRS ? (tiles + 1) / 2 : tiles)) return;
   const Tiles tile = tiles_of<PAIRS>(group, tiles);
-  const int kv_len = a.seqs.kv_len[b];
-  const int pos0 = kv_len - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
+  const int pos0 = a.seqs.kv_len[b] - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
+  const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
   const Blocks blocks =
       visible_blocks<BT>(pos0 + tile.first * ROWS / g,
                          pos0 + (min((tile.second + 1) * ROWS, pairs) - 1) / g, kv_len, a.window,
@@ -699,8 +706,9 @@ __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a) {
   if (r < row0) return;
   const int n = min(min(a.seqs.row_start[b + 1], a.seqs.n_rows) - row0, a.seqs.max_rows);
   if (r - row0 >= n) return;
-  const int g = a.group, kv_len = a.seqs.kv_len[b], tiles = (n * g + ROWS - 1) / ROWS;
-  const int pos0 = kv_len - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
+  const int g = a.group, tiles = (n * g + ROWS - 1) / ROWS;
+  const int pos0 = a.seqs.kv_len[b] - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
+  const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
   const Tiles tile =
       tiles_of<PAIRS>(group_of<PAIRS>(((r - row0) * g + head % g) / ROWS, tiles), tiles);
   const Blocks blocks =

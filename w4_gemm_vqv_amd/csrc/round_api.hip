@@ -205,11 +205,12 @@ vqv_status plan_attn(const vqv_cache* cache, const vqv_seqs* seqs, int heads, in
   if (!vqv::attn_dim_supported(cache->dim) || heads / cache->kv_heads > 1024)
     return VQV_ERR_UNSUPPORTED;
   if ((int64_t)seqs->max_rows * heads >= (1ll << 30) ||
-      (int64_t)seqs->n_rows * heads >= (1ll << 26))
+      (int64_t)seqs->n_rows * heads >= (1ll << 30))
     return VQV_ERR_UNSUPPORTED;
   *plan = vqv::attn_plan(*cache, *seqs, heads, window, sinks);
   if ((int64_t)cache->kv_heads * seqs->n_seqs * plan->groups * plan->splits >= (1ll << 23))
-    return VQV_ERR_UNSUPPORTED;
+    return VQV_ERR_UNSUPPORTED;  // threads of a grid are counted in 32 bits
+  if (plan->splits > 1 && (int64_t)seqs->n_rows * heads >= (1ll << 24)) return VQV_ERR_UNSUPPORTED;
   return VQV_OK;
 }
 

@@ -6,8 +6,8 @@ The classes hold a call's tensors and the struct that the library reads, made
 once; the functions carry the C names and only marshal arguments. The library
 sees pointers, so every tensor's device, type, size and layout is checked
 here. Calls go to the current stream unless `stream` names another (its
-handle, or a torch stream); a workspace that a call makes for itself is kept
-for that stream.
+handle, or a torch stream); what a call allocates, outputs or a workspace, then
+belongs to that stream.
 """
 
 from __future__ import annotations
@@ -119,16 +119,22 @@ def _take(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype,
     return t.data_ptr()
 
 
+def _new(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """An empty tensor that belongs to the call's stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _scratch(workspace: torch.Tensor | None, need: int, device: torch.device, stream) -> tuple:
     """(tensor, pointer, bytes) of the caller's workspace, or of one made here."""
     if workspace is None:
         if not need:
             return None, None, 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        if stream is not None:
-            if isinstance(stream, int):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            workspace.record_stream(stream)
+        workspace = _new(need, torch.uint8, device, stream)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a dense tensor on {device}")
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -273,7 +279,7 @@ def vqv_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pa
            *_rows(k, "k", (n, cache.kv_heads, cache.dim), q.dtype, dev),
            *_rows(v, "v", (n, cache.kv_heads, cache.dim), q.dtype, dev))
     if q_out is None:
-        q_out = torch.empty((n, heads, cache.dim), dtype=cache.dtype, device=dev)
+        q_out = _new((n, heads, cache.dim), cache.dtype, dev, stream)
     out = _take(q_out, "q_out", (n, heads, cache.dim), cache.dtype, dev)
     _check(_round_lib().vqv_rope_append(*ins, _DTYPES[q.dtype], heads, cache.c, layer, seqs.c,
                                         rope.c, out, _stream(stream, dev)))
@@ -299,7 +305,7 @@ def vqv_paged_attn(q: torch.Tensor, cache: PagedCache, seqs: Sequences, scale: f
     shape = (seqs.n_rows, heads, cache.dim)
     qp = _take(q, "q", shape, cache.dtype, dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new(shape, cache.dtype, dev, stream)
     op = _take(out, "out", shape, cache.dtype, dev)
     need = 0 if workspace is not None else vqv_paged_attn_workspace_bytes(cache, seqs, heads,
                                                                           window, sinks)
@@ -340,7 +346,7 @@ def vqv_cache_reserve(pages: Pages, goal_len: torch.Tensor, ok: torch.Tensor | N
     returns ok [rows] int32."""
     n, dev = goal_len.numel(), pages.device
     if ok is None:
-        ok = torch.empty(n, dtype=torch.int32, device=dev)
+        ok = _new(n, torch.int32, dev, stream)
     need = 0 if workspace is not None else vqv_cache_workspace_bytes(pages)
     workspace, wp, wn = _scratch(workspace, need, dev, stream)
     _check(_round_lib().vqv_cache_reserve(pages.c, _list(goal_len, "goal_len", n, dev), n,
@@ -356,7 +362,7 @@ def vqv_cache_fork(cache: PagedCache, pages: Pages, parent: torch.Tensor, child:
     n, dev = parent.numel(), pages.device
     _same(cache.device, pages=pages)
     if ok is None:
-        ok = torch.empty(n, dtype=torch.int32, device=dev)
+        ok = _new(n, torch.int32, dev, stream)
     need = 0 if workspace is not None else vqv_cache_workspace_bytes(pages)
     workspace, wp, wn = _scratch(workspace, need, dev, stream)
     _check(_round_lib().vqv_cache_fork(cache.c, pages.c, _list(parent, "parent", n, dev),
@@ -372,7 +378,7 @@ def vqv_cache_compact(cache: PagedCache, seqs: Sequences, keep: torch.Tensor,
     dev = cache.device
     _same(dev, seqs=seqs)
     if new_len is None:
-        new_len = torch.empty(seqs.n_seqs, dtype=torch.int32, device=dev)
+        new_len = _new(seqs.n_seqs, torch.int32, dev, stream)
     _check(_round_lib().vqv_cache_compact(cache.c, seqs.c, _list(keep, "keep", seqs.n_rows, dev),
                                           _list(new_len, "new_len", seqs.n_seqs, dev),
                                           _stream(stream, dev)))
@@ -400,7 +406,7 @@ def vqv_logits_edit(logits: torch.Tensor, edits: Edits, draft: torch.Tensor | No
     int32 bits of the allowed tokens."""
     dev, lp, dp, mp = _logits_in(logits, edits, draft, B, T, mask)
     if out is None:
-        out = torch.empty_like(logits)
+        out = _new(logits.shape, torch.float32, dev, stream)
     op = _take(out, "out", (B * T, edits.vocab), torch.float32, dev)
     _check(_round_lib().vqv_logits_edit(lp, edits.c, dp, T, mp, op, _stream(stream, dev)))
     return out
@@ -416,11 +422,11 @@ def vqv_logits_verify(logits: torch.Tensor, edits: Edits, draft: torch.Tensor | 
     the edited logits, which are not written."""
     dev, lp, dp, mp = _logits_in(logits, edits, draft, B, T, mask)
     if argmax is None:
-        argmax = torch.empty(B * T, dtype=torch.int32, device=dev)
+        argmax = _new(B * T, torch.int32, dev, stream)
     if accept_len is None:
-        accept_len = torch.empty(B, dtype=torch.int32, device=dev)
+        accept_len = _new(B, torch.int32, dev, stream)
     if margin is None and want_margin:
-        margin = torch.empty(B * T, dtype=torch.float32, device=dev)
+        margin = _new(B * T, torch.float32, dev, stream)
     need = 0 if workspace is not None else vqv_verify_workspace_bytes(B, T, edits.vocab)
     workspace, wp, wn = _scratch(workspace, need, dev, stream)
     _check(_round_lib().vqv_logits_verify(
