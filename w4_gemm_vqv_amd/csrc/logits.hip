@@ -12,7 +12,11 @@
 // Every step is one rounding in fp32 (no contraction to a fused
 // multiply-add), so a token is chosen as the formulas choose it.
 //
-// The bound is memory: logits once (and once out), counts once per sequence.
+// The floor is memory: logits once (and once out), counts once per sequence.
+// 64 rows over 151936 tokens with all edits and the verify take 30 us, 8.8 of
+// them the floor: 53 vector instructions per token and row keep the vector
+// units busy 40 % of the time, and the loads that follow one another at a
+// work-group's start (biases, counts, the first row) take most of the rest.
 
 #include "argmax.h"
 #include "round_internal.h"
@@ -175,7 +179,8 @@ __global__ __launch_bounds__(kThreads) void logits_edit(const EditArgs a) {
 }
 
 // Rows of a work-group: all of a sequence's, so that its counts are read
-// once, unless that leaves fewer than two work-groups for a CU.
+// once, unless that leaves fewer than two work-groups for a CU (4 sequences of
+// 16 rows: 4 rows, 30.1 us; 2 rows, 32.3).
 int rows_per_group(int B, int T, int tiles) {
   int rows = T;
   while (rows > 1 && (int64_t)B * tiles * ((T + rows - 1) / rows) < 512) rows = (rows + 1) / 2;

