@@ -30,7 +30,7 @@
 // needs no exchange at all.
 //
 // Softmax runs with base-2 exponentials and a running maximum; scores, maxima,
-// sums and outputs are fp32. P is rounded to the cache's type, the matrix
+// sums and outputs are fp32. P (at most 2^8) is rounded to the cache's type, the matrix
 // instruction's input: an error of at most half a step of each weight, which
 // the sum over tokens averages.
 
