@@ -137,8 +137,9 @@ vqv_status vqv_rope_append(const void* q, int64_t q_row_stride, int64_t q_head_s
  *   dim        64, 80, 96, 128, 192 or 256 (else VQV_ERR_UNSUPPORTED).
  *   workspace  vqv_paged_attn_workspace_bytes bytes, 16-byte aligned; may be
  *              NULL when that is 0. Its contents on entry do not matter.
- * Scores, maxima, sums and the output are held in fp32; the weights p_j
- * are rounded to the cache's type (half a step each) for the product with v.
+ * Scores, maxima, sums and the output are held in fp32; the weights p_j,
+ * relative to the largest so far, are rounded to the cache's type (half a step
+ * each, the largest is exact) for the product with v.
  */
 size_t vqv_paged_attn_workspace_bytes(const vqv_cache* cache, const vqv_seqs* seqs, int heads,
                                       int window, int sinks);

@@ -264,3 +264,46 @@ def test_refuses_wrong_tensors(vqv):
         vqv.vqv_paged_attn(c.qd, c.cache, c.seqs, scale=1.0, out=torch.empty(2, 2, 64, device="cuda"))
     with pytest.raises(vqv.VqvError):
         vqv.vqv_paged_attn(c.qd, c.cache, c.seqs, scale=0.0)
+
+
+def near(c, got, want, low=0.0):
+    """As `close`, for scores of one product each, where the largest weight of a wave's tokens is 1
+    exactly (`want`'s mean is then what the others come to) and fp16 weights are 2^15 times as
+    large: off by up to 2^-25 of that where they are subnormal; low is the sum of |v| over tokens."""
+    out, mean, size = want
+    half, n = torch.finfo(c.t).eps / 2, max(c.kv)
+    score = size * 9 * 2.0 ** -24 + 2.0 ** -22
+    inner = (2 * score + (n + 8) * 2.0 ** -24) * torch.maximum(mean, out.abs()) + half * mean
+    if c.t == torch.float16:
+        inner = inner + 2.0 ** -40 * low
+    allow = half * (out.abs() + inner) + inner + 2.0 ** -25
+    err = (got.double() - out).abs()
+    assert (err <= allow).all(), f"error over allowance {(err / allow).nan_to_num(1e9).max():.3g}"
+
+
+def ladder(rows, dim, dtype, steps, heads=2, seed=0, kv=1300):
+    """A case whose scores go by the first column alone: step (token, score of a row of factor 1);
+    all other tokens score -30 times that. Row i's factor is between 1 and 1.5. One split."""
+    c = Case(rows=[rows], kv=[kv], heads=heads, hk=1, dim=dim, ps=16, dtype=dtype, seed=seed, max_kv=64)
+    c.q.zero_()
+    c.q[:, :, 0] = (1 + torch.rand(rows, heads, generator=torch.Generator().manual_seed(seed)) / 2).to(c.t)
+    c.k[0, c.table[0][:-(-kv // 16)], :, :, 0] = -30.0
+    for t, score in steps:
+        c.k[0, c.table[0][t // 16], t % 16, :, 0] = score
+    c.k[0, :, :, :, 1:] = 0
+    return c
+
+
+SHAPES_OF_WAVES = [(2, 64), (2, 128), (2, 256), (20, 80), (20, 192), (50, 96), (50, 192), (100, 64), (100, 128)]
+
+
+@pytest.mark.parametrize("rows,dim", SHAPES_OF_WAVES)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_largest_weight_is_exact(vqv, rows, dim, dtype):
+    """A score that passes the one before it by less than 2^8 (in a later block of the same wave)
+    has the largest weight: its error is none, and the other's is multiplied by values of 0."""
+    c = ladder(rows, dim, dtype, [(0, 1.0), (512, 3.5)])
+    c.v[0, c.table[0][0], 0] = 0
+    out, mean, size = c.want(scale=1.0)
+    # all of the sum of weighted |v| but for the largest weight's part
+    near(c, c.run(vqv, scale=1.0), (out, (mean - out.abs()).clamp(min=0), size))
