@@ -139,7 +139,8 @@ vqv_status vqv_rope_append(const void* q, int64_t q_row_stride, int64_t q_head_s
  *              NULL when that is 0. Its contents on entry do not matter.
  * Scores, maxima, sums and the output are held in fp32; the weights p_j,
  * relative to the largest so far, are rounded to the cache's type (half a step
- * each, the largest is exact) for the product with v.
+ * each, the largest is exact; in fp16 those 2^29 below the largest by up to
+ * 2^-40 of it) for the product with v and for their sum.
  */
 size_t vqv_paged_attn_workspace_bytes(const vqv_cache* cache, const vqv_seqs* seqs, int heads,
                                       int window, int sinks);

@@ -307,3 +307,37 @@ def test_largest_weight_is_exact(vqv, rows, dim, dtype):
     out, mean, size = c.want(scale=1.0)
     # all of the sum of weighted |v| but for the largest weight's part
     near(c, c.run(vqv, scale=1.0), (out, (mean - out.abs()).clamp(min=0), size))
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 256), (50, 192), (100, 64), (100, 128), (100, 256)])
+@pytest.mark.parametrize("below", [11.0, 17.5, 21.0])
+def test_many_small_weights(vqv, rows, dim, below):
+    """fp16: thousands of tokens far below one of values 0 are most of the output."""
+    c = Case(rows=[rows], kv=[6000], heads=1, hk=1, dim=dim, ps=16, dtype="fp16", max_kv=64)
+    c.q.zero_()
+    c.q[:, :, 0] = 1.0
+    c.k.zero_()
+    c.k[0, c.table[0][0], 3, :, 0] = below
+    c.v[0, c.table[0][:375]] = 500 + 100 * c.v[0, c.table[0][:375]]
+    c.v[0, c.table[0][0], 3] = 0
+    low = c.v[0, c.table[0][:375]].double().abs().sum((0, 1, 2))
+    near(c, c.run(vqv, scale=1.0), c.want(scale=1.0), low=low)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,dim", [(2, 64), (50, 192), (100, 64), (300, 128)])
+def test_seen_nan_and_infinity_in_every_shape(vqv, rows, dim, dtype):
+    """A NaN among the keys, and a score of infinity: NaN; an infinity among the values of a seen
+    token comes out, in its column alone."""
+    c = Case(rows=[rows], kv=[400], heads=2, hk=1, dim=dim, ps=16, dtype=dtype)
+    p, clean = c.table[0][1], c.run(vqv)
+    for x in (float("nan"), float("inf")):
+        keep = c.k[0, p, 3].clone()
+        c.k[0, p, 3, 0, 5] = x
+        got = c.run(vqv)
+        assert got[c.q[:, :, 5] * x != -float("inf")].isnan().all()
+        c.k[0, p, 3] = keep
+    c.v[0, p, 3, 0, 7] = -float("inf")
+    got = c.run(vqv)
+    assert (got[:, :, 7] == -float("inf")).all()
+    assert torch.equal(got[:, :, :7], clean[:, :, :7]) and torch.equal(got[:, :, 8:], clean[:, :, 8:])

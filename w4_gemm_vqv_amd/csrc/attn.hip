@@ -30,9 +30,11 @@
 // needs no exchange at all.
 //
 // Softmax runs with base-2 exponentials and a running maximum; scores, maxima,
-// sums and outputs are fp32. P (at most 1) is rounded to the cache's type, the matrix
-// instruction's input: an error of at most half a step of each weight, none of
-// the largest, which the sum over tokens averages.
+// sums and outputs are fp32. P is rounded to the cache's type, the matrix instruction's
+// input: an error of at most half a step of each weight, none of the largest,
+// which the sum over tokens averages. The largest is 1, in fp16 2^15 (the sum
+// of weights is as much larger): with 1 a token 2^14 below it would lose bits,
+// and thousands of them 2^25 below would be nothing.
 
 #include <limits.h>
 
@@ -91,15 +93,33 @@ __device__ __forceinline__ unsigned pack2(float a, float b) {
 }
 
 template <typename T>
-struct Bits;  // of a type: its exponent, and 1
+struct Bits;  // of a type: its exponent, 1, and log2 of the largest weight
 template <>
 struct Bits<__bf16> {
   static constexpr unsigned exponent = 0x7F80u, one = 0x3F80u;
+  static constexpr float top = 0.0f;
 };
 template <>
 struct Bits<_Float16> {
   static constexpr unsigned exponent = 0x7C00u, one = 0x3C00u;
+  static constexpr float top = 15.0f;
 };
+
+// c + both values of w, in fp32.
+template <typename T>
+__device__ __forceinline__ float add2(unsigned w, float c);
+template <>
+__device__ __forceinline__ float add2<__bf16>(unsigned w, float c) {
+  typedef __attribute__((ext_vector_type(2))) __bf16 t2;
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(t2, w),
+                                         t2{(__bf16)1.0f, (__bf16)1.0f}, c, false);
+}
+template <>
+__device__ __forceinline__ float add2<_Float16>(unsigned w, float c) {
+  typedef __attribute__((ext_vector_type(2))) _Float16 t2;
+  return __builtin_amdgcn_fdot2(__builtin_bit_cast(t2, w),
+                                t2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+}
 
 // Not 0 where one of two packed values is an infinity or NaN: an exponent of
 // ones carries into the sign's place.
@@ -570,20 +590,20 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= back;
     }
-    const float shift = mx == -__builtin_inff() ? 0.0f : mx * a.scale_log2;
-    // The weights of 16 tokens, as the B operand of their product.
+    const float shift = fmaf(mx == -__builtin_inff() ? 0.0f : mx, a.scale_log2, -Bits<T>::top);
+    // The weights of 16 tokens, as the B operand of their product. The sum
+    // takes them as rounded, as the product does.
     const auto weights = [&](int u) {
       u32x4 w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float p[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < 2; ++e)
           p[e] = __builtin_amdgcn_exp2f(
               fmaf(s[u / 2][8 * (u & 1) + 2 * i + e], a.scale_log2, -shift));
-          sum += p[e];
-        }
         w[i] = pack2<T>(p[0], p[1]);
+        sum = add2<T>(w[i], sum);
       }
       return __builtin_bit_cast(s16x8, w);
     };
