@@ -341,3 +341,17 @@ def test_seen_nan_and_infinity_in_every_shape(vqv, rows, dim, dtype):
     got = c.run(vqv)
     assert (got[:, :, 7] == -float("inf")).all()
     assert torch.equal(got[:, :, :7], clean[:, :, :7]) and torch.equal(got[:, :, 8:], clean[:, :, 8:])
+
+
+@pytest.mark.parametrize("rows,dim", SHAPES_OF_WAVES)
+def test_scores_past_any_exponent(vqv, rows, dim):
+    """Scores of 1e6 to 1e37: one token takes all, and the output is its values."""
+    for size in (1e6, 1e10, 1e20, 1e34):
+        c = ladder(rows, dim, "bf16", [(t, 2.0 ** (t / 100) * size) for t in range(0, 1200, 37)], kv=1300)
+        for sign in (1, -1):
+            c.k[0, :, :, :, 0] *= sign
+            got, want = c.run(vqv, scale=1.0), c.want(scale=1.0)
+            if sign > 0:
+                assert torch.equal(got.double(), want[0])
+            else:   # the many tokens at 30 to 45, of equal weights
+                near(c, got, (want[0], want[1], torch.tensor(45.0)))

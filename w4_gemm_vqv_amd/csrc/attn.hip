@@ -54,6 +54,7 @@ typedef __attribute__((ext_vector_type(16))) float f32x16;
 typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 constexpr unsigned kNoPlace = ~0u;
+constexpr float kLarge = 4096.0f;  // a shift below it is off by 2^-13 at most
 
 struct AttnArgs {
   const void* q;
@@ -590,7 +591,17 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] *= back;
     }
-    const float shift = fmaf(mx == -__builtin_inff() ? 0.0f : mx, a.scale_log2, -Bits<T>::top);
+    const float base = mx == -__builtin_inff() ? 0.0f : mx;
+    float shift = fmaf(base, a.scale_log2, -Bits<T>::top);
+    // Of a large maximum the shift's rounding would be the weights' size: the
+    // maximum is then taken off the scores first, which is exact near it.
+    if (__any(fabsf(shift) > kLarge)) {
+      shift = -Bits<T>::top;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[u][i] -= base;
+    }
     // The weights of 16 tokens, as the B operand of their product. The sum
     // takes them as rounded, as the product does.
     const auto weights = [&](int u) {
