@@ -355,3 +355,14 @@ def test_scores_past_any_exponent(vqv, rows, dim):
                 assert torch.equal(got.double(), want[0])
             else:   # the many tokens at 30 to 45, of equal weights
                 near(c, got, (want[0], want[1], torch.tensor(45.0)))
+
+
+@pytest.mark.parametrize("rows,kv", [(8, 5), (8, 1), (50, 20), (150, 100)])
+def test_window_past_any_length(vqv, rows, kv):
+    """The widest window, also where the first rows stand before the first token."""
+    c = Case(rows=[rows, rows], kv=[kv, kv + 30], heads=2, hk=1, dim=64, ps=16)
+    plain = c.run(vqv)
+    for window in (2 ** 31 - 1, 2 ** 31 - kv, 2 ** 30 + 1):
+        for sinks in (0, 3, 2 ** 31 - 1):
+            c.close(c.run(vqv, window, sinks), c.want())
+    c.close(plain, c.want())

@@ -317,6 +317,8 @@ __device__ __attribute__((noinline)) void product_with_bad_values(
 
 // The tokens that the rows of a tile see, as blocks of BT tokens: `sink`
 // blocks from token 0 on, then those from block `first` on; `all` in total.
+// Rows before the first token (a sequence shorter than its rows) see nothing;
+// with the widest window their lower bound would pass 32 bits.
 struct Blocks {
   int sink, first, all;
 };
@@ -326,7 +328,7 @@ __device__ __forceinline__ Blocks visible_blocks(int p0, int p1, int kv_len, int
                                                  int sinks) {
   const int hi = p1 < kv_len ? p1 + 1 : kv_len;
   if (hi <= 0) return Blocks{0, 0, 0};
-  const int lo = window > 0 ? min(max(p0 - window + 1, 0), hi) : 0;
+  const int lo = window > 0 ? min(max(max(p0, 0) - window + 1, 0), hi) : 0;
   const int sink_end = min(sinks, lo);
   Blocks r;
   r.sink = window > 0 && sink_end > 0 ? (sink_end + BT - 1) / BT : 0;
@@ -532,7 +534,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
     const int t0 = base_of(j) + kw * KT;
     // Nothing to see for these rows.
     if (t0 > p1 || m0 >= pairs ||
-        (a.window > 0 && t0 + KT <= p0 - a.window + 1 && t0 >= a.sinks))
+        (a.window > 0 && t0 + KT <= max(p0, 0) - a.window + 1 && t0 >= a.sinks))
       continue;
 
     f32x16 s[SUB];
@@ -554,7 +556,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
       // Token t0 + 32 u + 8 (i / 4) + 4 half + i % 4, against the row's bounds.
       const int l = lane_here(), row = (m0 + (l & 31)) / g, half = l >> 5;
       const int hi = (m0 + (l & 31) < pairs ? pos0 + row : -1) - t0 - 4 * half;
-      const int lo = a.window > 0 ? hi - a.window : INT_MIN;
+      const int lo = a.window > 0 ? max(hi, -1) - a.window : INT_MIN;
       const int sink = a.sinks - t0 - 4 * half;
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
@@ -846,7 +848,7 @@ AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window,
   if (window > 0) {
     const int64_t rows_of_tile = 32 * p.mw / (heads / c.kv_heads) + 2;
     int64_t seen = (int64_t)window + rows_of_tile + 2 * bt;
-    seen += sinks < s.max_kv ? sinks + bt : s.max_kv;
+    seen += sinks < s.max_kv ? (int64_t)sinks + bt : s.max_kv;
     tokens = seen < tokens ? seen : tokens;
   }
   const int blocks = ceil_div(tokens < 1 ? 1 : tokens, bt);
