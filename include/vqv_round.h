@@ -179,8 +179,9 @@ vqv_status vqv_cache_copy(const vqv_cache* cache, const int32_t* src, const int3
  * Gives back the pages of table rows past keep_len tokens: for each row i of
  * the n (row rows[i], or i when rows is NULL, then n <= pages->rows) the
  * pages from ceil(keep_len[i] / page_size) on lose one reference and leave
- * the table; held and length are cut. A negative length is 0; a longer one
- * than the row's changes nothing; a row outside the table is left out.
+ * the table; held and length are cut, and never grow. A negative length is 0;
+ * a row outside the table is left out; of a row that is named several times
+ * the shortest length counts.
  */
 vqv_status vqv_cache_trim(const vqv_pages* pages, const int32_t* keep_len, const int32_t* rows,
                           int n, void* hip_stream);

@@ -135,6 +135,22 @@ def test_trim_named_rows(vqv):
     dev.check(book)
 
 
+@pytest.mark.parametrize("order", ["as drawn", "rising", "falling"])
+def test_trim_rows_named_with_other_lengths(vqv, order):
+    """A row that is named several times is cut to the shortest of its lengths, whatever the order."""
+    for seed in range(20):
+        gen = torch.Generator().manual_seed(seed)
+        book = random_book(seed, 6, 40, 4, 400)
+        dev = Device(vqv, book)
+        keep = torch.randint(60, 170, (600,), generator=gen)
+        if order != "as drawn":
+            keep = keep.sort(descending=order == "falling").values
+        rows = torch.randint(-1, 7, (600,), generator=gen).tolist()
+        vqv.vqv_cache_trim(dev.pages, keep.to(torch.int32).cuda(), rows=i32(rows))
+        book.trim(keep.tolist(), rows)
+        dev.check(book)
+
+
 def test_trim_bad_pages(vqv):
     """Entries that name no page leave the table and touch nothing."""
     book = ref.Book([1, 1, 0], [[0, 99, -7, 1]], [4], [60], 16)

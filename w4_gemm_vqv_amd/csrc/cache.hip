@@ -121,8 +121,9 @@ __device__ __forceinline__ int clamp_int(int x, int lo, int hi) {
   return x < lo ? lo : x > hi ? hi : x;
 }
 
-// One wave per row. A page leaves the table by an exchange, so a row that is
-// named twice gives each page back once.
+// One wave per entry. A row may be named several times, with lengths of its
+// own: a page leaves the table by an exchange, so that it is given back once,
+// and held and length come to the shortest by atomic minima, in any order.
 __global__ __launch_bounds__(64) void cache_trim(const vqv_pages pg,
                                                  const int32_t* __restrict__ keep_len,
                                                  const int32_t* __restrict__ rows) {
@@ -139,8 +140,8 @@ __global__ __launch_bounds__(64) void cache_trim(const vqv_pages pg,
     if ((unsigned)p < (unsigned)pg.pages) atomicSub(&pg.ref[p], 1);
   }
   if (threadIdx.x == 0) {
-    if (stay < held) pg.held[row] = stay;
-    if (keep < length) pg.length[row] = keep;
+    if (stay < held) atomicMin(&pg.held[row], stay);
+    if (keep < length) atomicMin(&pg.length[row], keep);
   }
 }
 
