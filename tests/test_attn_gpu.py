@@ -366,3 +366,18 @@ def test_window_past_any_length(vqv, rows, kv):
         for sinks in (0, 3, 2 ** 31 - 1):
             c.close(c.run(vqv, window, sinks), c.want())
     c.close(plain, c.want())
+
+
+def test_no_rows(vqv):
+    """A call without rows is a call: of attention, of the append, of compact."""
+    c = Case(rows=[2, 1], kv=[20, 7], heads=4, hk=2, dim=64, ps=16)
+    c.run(vqv)
+    seqs = vqv.Sequences(i32([0, 0, 0]), i32([20, 7]), i32(c.table), n_rows=0, max_rows=0, max_kv=20)
+    before = [c.cache.k.clone(), c.cache.v.clone()]
+    q = torch.empty(0, 4, 64, dtype=c.t, device="cuda")
+    assert vqv.vqv_paged_attn(q, c.cache, seqs, scale=1.0).shape == (0, 4, 64)
+    k = torch.empty(0, 2, 64, dtype=c.t, device="cuda")
+    assert vqv.vqv_rope_append(q, k, k, c.cache, seqs, vqv.Rope(64)).shape == (0, 4, 64)
+    assert vqv.vqv_cache_compact(c.cache, seqs, i32([])).tolist() == [20, 7]
+    for x, y in zip((c.cache.k, c.cache.v), before):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))

@@ -158,6 +158,28 @@ def test_attn_grid_limits(R, L):
     assert attn_call(R, L, s=seqs(R, n_rows=1 << 20, n_seqs=1), heads=32, wn=1 << 60) == UNSUP
 
 
+def test_empty_calls(R, L):
+    """No rows: no memory is needed for them, as of an empty tensor. What else is wrong is refused."""
+    none = seqs(R, n_rows=0)
+    rows = dict(q=None, k=None, v=None, out=None)
+    assert rope_call(R, L, s=none, **rows) == OK
+    assert rope_call(R, L, s=none, q=None) == OK
+    assert rope_call(R, L, s=none, layer=2, **rows) == ARG
+    assert rope_call(R, L, s=none, rot=256, **rows) == ARG
+    assert rope_call(R, L, s=seqs(R), out=None) == ARG
+    assert attn_call(R, L, s=none, q=None, out=None, ws=None, wn=0) == OK
+    assert attn_call(R, L, s=none, q=None, out=None, ws=None, wn=0, scale=0.0) == ARG
+    assert attn_call(R, L, s=none, q=None, out=None, ws=None, wn=0, heads=33) == ARG
+    assert attn_call(R, L, s=seqs(R, max_rows=0), q=None) == ARG
+    # pages and lists of none
+    p = pages(R)
+    need = L.vqv_cache_workspace_bytes(p)
+    assert L.vqv_cache_copy(cache(R), None, None, 0, None) == OK
+    assert L.vqv_cache_trim(p, None, None, 0, None) == OK
+    assert L.vqv_cache_reserve(p, None, 0, None, P[8], need, None) == OK
+    assert L.vqv_cache_fork(cache(R), p, None, None, 0, None, P[8], need, None) == OK
+
+
 def test_attn_dims(R, L):
     for d in (8, 72, 136, 248):
         assert attn_call(R, L, c=cache(R, dim=d)) == UNSUP

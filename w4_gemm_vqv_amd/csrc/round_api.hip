@@ -159,7 +159,8 @@ vqv_status vqv_rope_append(const void* q, int64_t q_row_stride, int64_t q_head_s
   vqv_status st = check_cache(cache);
   if (st != VQV_OK) return st;
   if ((st = check_seqs(seqs)) != VQV_OK) return st;
-  if (!q || !k || !v || !rope || !q_out) return VQV_ERR_ARG;
+  // The rows of an empty call may have no memory at all.
+  if (!rope || (seqs->n_rows && (!q || !k || !v || !q_out))) return VQV_ERR_ARG;
   if (in_dtype != VQV_BF16 && in_dtype != VQV_FP16 && in_dtype != VQV_FP32) return VQV_ERR_ARG;
   if (heads < 1 || layer < 0 || layer >= cache->layers) return VQV_ERR_ARG;
   if (rope->rot < 2 || rope->rot % 2 || rope->rot > 256 || rope->rot > cache->dim)
@@ -231,7 +232,7 @@ vqv_status vqv_paged_attn(const void* q, const vqv_cache* cache, int layer, cons
   vqv::AttnPlan plan;
   const vqv_status st = plan_attn(cache, seqs, heads, window, sinks, &plan);
   if (st != VQV_OK) return st;
-  if (!q || !out || layer < 0 || layer >= cache->layers) return VQV_ERR_ARG;
+  if ((seqs->n_rows && (!q || !out)) || layer < 0 || layer >= cache->layers) return VQV_ERR_ARG;
   if (!(scale > 0.0f) || !isfinite(scale)) return VQV_ERR_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return VQV_ERR_ALIGN;
   const size_t bytes = (size_t)seqs->n_rows * heads * cache->dim * 2;
