@@ -204,7 +204,9 @@ vqv_status vqv_cache_reserve(const vqv_pages* pages, const int32_t* goal_len, in
  * lowest free numbers first), all layers, k and v. held and length are the
  * parent's, cut to its last token's page. ok[i] is 1, or 0 where nothing was
  * done: a row outside the table, a child that holds pages, is named twice
- * (the first stands) or is a parent of this call, or no page free for it.
+ * (the first stands) or is a parent of this call, a parent whose last, partly
+ * filled page is none of the cache, or no page free for it. Entries of full
+ * pages that are none are passed on as they are.
  */
 vqv_status vqv_cache_fork(const vqv_cache* cache, const vqv_pages* pages, const int32_t* parent,
                           const int32_t* child, int n, int32_t* ok, void* workspace,

@@ -149,12 +149,13 @@ class Book:
             full, rest = divmod(self.length[p], self.ps)
             full = min(full, self.held[p])
             part = rest != 0 and self.held[p] > full
-            if part and not free:
+            if part and (not 0 <= self.table[p][full] < len(self.ref) or not free):
                 ok.append(0)
                 continue
             for j in range(full):
                 self.table[c][j] = self.table[p][j]
-                self.ref[self.table[p][j]] += 1
+                if 0 <= self.table[p][j] < len(self.ref):
+                    self.ref[self.table[p][j]] += 1
             if part:
                 new = free.pop(0)
                 self.ref[new] = 1

@@ -229,6 +229,24 @@ def test_fork_refused_pairs(vqv):
     dev.check(book)
 
 
+@pytest.mark.parametrize("bad", [-1, 6, 1 << 30])
+def test_fork_bad_pages(vqv, bad):
+    """A parent whose last page is none has no branch (its tokens there are hidden; a new page
+    would show another sequence's); an entry of a full page that is none is passed on."""
+    ps, none = 4, [-1] * 3
+    table = [[0, bad, -1], [bad, 2, -1], none[:], none[:], none[:]]
+    book = ref.Book([1, 0, 1, 0, 0, 0], table, [2, 2, 0, 0, 0], [6, 7, 0, 0, 0], ps)
+    cache, dev = pair(vqv, (1, ps, 1, 8, torch.bfloat16, "slot"), 6), Device(vqv, book)
+    want = [bits(x) for x in (cache.k, cache.v)]
+    ok = vqv.vqv_cache_fork(cache, dev.pages, i32([0, 1]), i32([2, 3]))
+    good, copies = book.fork([0, 1], [2, 3])
+    assert ok.tolist() == good == [0, 1] and copies == [(2, 1)]
+    dev.check(book)
+    for x, got in zip(want, (cache.k, cache.v)):
+        x[:, 1] = x[:, 2]
+        assert torch.equal(bits(got), x)
+
+
 def compact(vqv, shape, rows, kv, keep, bad=()):
     layers, ps, hk, dim, dtype, layout = shape
     start = [0]

@@ -236,9 +236,10 @@ __global__ __launch_bounds__(kBook) void cache_fork_book(
         const int length = max(pg.length[p], 0);
         const int full = length / pg.page_size;
         if (length % pg.page_size && full < held) {
-          need = 1;
           old = pg.table[(int64_t)p * pg.width + full];
-          if ((unsigned)old >= (unsigned)pg.pages) old = -1;
+          good = (unsigned)old < (unsigned)pg.pages;
+          need = good;
+          if (!good) old = -1;
         }
       }
       ok[i] = good;
