@@ -151,7 +151,9 @@ vqv_status vqv_paged_attn(const void* q, const vqv_cache* cache, int layer, cons
 
 /*
  * The book of a cache's pages.
- *   ref        [pages] int32: tables that hold the page; 0: free.
+ *   ref        [pages] int32: tables that hold the page; 0: free. Nothing is
+ *              to be written to a page that several hold (vqv_rope_append and
+ *              vqv_cache_compact do not see the book and cannot tell).
  *   table      [rows, width] int32, rows width apart; -1 where none.
  *   held       [rows] int32: pages of a row, table[row][0 .. held-1].
  *   length     [rows] int32: tokens of a row.
@@ -191,8 +193,12 @@ vqv_status vqv_cache_trim(const vqv_pages* pages, const int32_t* keep_len, const
  * (all pages->rows rows, or the first n). Rows are served in their order, a
  * row's pages in theirs, from the free pages in the order of their numbers.
  * ok[i] (int32) is 1, or 0 for a row that got none: its goal is wider than
- * the table, or the free pages do not reach for it (and then not for any row
- * after it that needs some). `length` is not changed.
+ * the table, its goal is past `length` and token `length` falls on a page that
+ * other rows hold too, or the free pages do not reach for it (and then not for
+ * any row after it that needs some). `length` is not changed.
+ *   Such a page is left by a trim to inside the pages that a row shares with
+ *   its branches. To go on from there, fork the row once more (the branch gets
+ *   a copy of its own of that page), trim the row to 0 and use the branch.
  */
 vqv_status vqv_cache_reserve(const vqv_pages* pages, const int32_t* goal_len, int n, int32_t* ok,
                              void* workspace, size_t workspace_bytes, void* hip_stream);

@@ -123,6 +123,12 @@ class Book:
             if want > self.width:
                 ok.append(0)
                 continue
+            last = self.length[r] // self.ps
+            if n > self.length[r] and last < self.held[r]:
+                p = self.table[r][last]
+                if 0 <= p < len(self.ref) and self.ref[p] > 1:
+                    ok.append(0)
+                    continue
             need = max(want - self.held[r], 0)
             if need and (short or need > len(free)):
                 short = True

@@ -212,6 +212,44 @@ def test_fork(vqv, shape):
         dev.check(book)
 
 
+@pytest.mark.parametrize("extra", [0, 1500])
+def test_reserve_on_shared_pages(vqv, extra):
+    """A branch that is cut inside the pages that it shares gets no room to write there; a branch of
+    the branch does, and what is appended to it does not reach the first row. extra: rows more than
+    the book's work-group has threads."""
+    ps, width, pages = 16, 8, 20
+    book = ref.Book([1, 1, 1] + [0] * (pages - 3), [[2, 0, 1] + [-1] * 5] + [[-1] * width for _ in range(4 + extra)],
+                    [3] + [0] * (4 + extra), [40] + [0] * (4 + extra), ps)
+    cache, dev = pair(vqv, (2, ps, 1, 64, torch.bfloat16, "slot"), pages), Device(vqv, book)
+    tail = [0] * extra
+
+    def both(name, *a):
+        got = getattr(vqv, "vqv_cache_" + name)(*([cache] if name == "fork" else []), dev.pages, *map(i32, a))
+        want = getattr(book, name)(*a)
+        if name != "trim":
+            assert got.tolist() == (want[0] if name == "fork" else want)
+        dev.check(book)
+        return want
+
+    both("fork", [0, 0, 0], [1, 2, 3])
+    both("trim", [20, 32, 40], [1, 2, 3])
+    # row 1 ends in a shared page, row 2 at its border, row 3 in its own; row 1 may keep what it has
+    assert both("reserve", [56, 21, 33, 41, 0] + tail)[:5] == [1, 0, 1, 1, 1]
+    assert both("reserve", [56, 20, 33, 41, 0] + tail)[:5] == [1, 1, 1, 1, 1]
+    before = [bits(x) for x in (cache.k, cache.v)]
+    both("fork", [1], [4])
+    both("trim", [0], [1])
+    assert both("reserve", [40, 0, 33, 41, 21] + tail)[:5] == [1, 1, 1, 1, 1]
+    x = torch.ones(1, 1, 64, device="cuda", dtype=torch.bfloat16)
+    seqs = vqv.Sequences(i32([0, 0, 0, 0, 0, 1]), i32([40, 0, 32, 40, 21]), dev.t[1], n_rows=1, max_rows=1, max_kv=48)
+    vqv.vqv_rope_append(x, x, x, cache, seqs, vqv.Rope(64), layer=1)
+    torch.cuda.synchronize()
+    held = [p for r in (0, 2, 3) for p in book.table[r] if p >= 0]
+    for got, w in zip((cache.k, cache.v), before):
+        assert torch.equal(bits(got)[:, held], w[:, held])
+    assert (cache.v[1, book.table[4][1], 4] == 1).all()
+
+
 def test_fork_refused_pairs(vqv):
     """Rows that are none, a child that holds pages, is named twice or is a
     parent, and too few free pages."""
