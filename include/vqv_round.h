@@ -263,7 +263,8 @@ typedef struct {
 /*
  * out = edited logits [B*T, n] fp32; out may be logits itself (no other
  * overlap). draft as in vqv_verify (NULL: none are counted), mask int32
- * [B*T, ceil(n/32)] or NULL. B = edits->n_seqs, 1 <= T <= 64, B*T*n < 2^31.
+ * [B*T, ceil(n/32)] or NULL. B = edits->n_seqs, 1 <= T <= 64, B*T*n < 2^31,
+ * n <= 2^31 - 4096 (else VQV_ERR_UNSUPPORTED).
  * 16-byte aligned logits and out.
  */
 vqv_status vqv_logits_edit(const float* logits, const vqv_edits* edits, const int32_t* draft,

@@ -259,6 +259,15 @@ def test_edits_refusals(R, L, kw, T, status):
                                None) == status
 
 
+@pytest.mark.parametrize("n", [2 ** 31 - 1, 2 ** 31 - 32, 2 ** 31 - 4095])
+def test_edits_past_the_last_tile(R, L, n):
+    """Tokens of the last tile that 32 bits do not count."""
+    a = [i << 40 for i in range(1, 8)]   # far enough apart
+    e = R._Edits(n_seqs=1, n=n)
+    assert L.vqv_logits_edit(a[0], e, None, 1, a[1], a[2], None) == UNSUP
+    assert L.vqv_logits_verify(a[0], e, None, None, 1, a[1], a[2], a[3], None, a[4], 1 << 39, None) == UNSUP
+
+
 def test_logits_refusals(R, L):
     e = edits(R)
     ed = lambda *a: L.vqv_logits_edit(*a, None)

@@ -68,7 +68,8 @@ vqv_status check_edits(const vqv_edits* e, int T) {
   if (!e || e->n_seqs < 1 || e->n < 1 || T < 1 || T > 64 || e->n_bias < 0) return VQV_ERR_ARG;
   if ((double)e->n_seqs * T * e->n >= 2147483648.0) return VQV_ERR_ARG;
   if (e->bias_start && e->n_bias && (!e->bias_token || !e->bias_value)) return VQV_ERR_ARG;
-  if (e->n_seqs > 65535) return VQV_ERR_UNSUPPORTED;
+  // The last tile's tokens are counted in 32 bits.
+  if (e->n_seqs > 65535 || e->n > INT32_MAX - (vqv::kVerifyChunk - 1)) return VQV_ERR_UNSUPPORTED;
   if (!words_aligned(e->counts, e->seen, e->repetition, e->frequency, e->presence, e->bias_start,
                      e->bias_token, e->bias_value))
     return VQV_ERR_ALIGN;
