@@ -81,7 +81,7 @@ typedef struct {
  *     VQV_ROPE_YARN    between f_i and f_i / factor along a ramp from the
  *                      pair that makes 32 turns in original_len positions
  *                      (floor) to the one that makes 1 (ceiling);
- *                      mscale = 0.1 ln(factor) + 1
+ *                      mscale = 0.1 ln(factor) + 1, or 1 where factor <= 1
  *     VQV_ROPE_SMOOTH  f_i where a pair makes 4 turns or more in
  *                      original_len, f_i / factor where it makes 1 or less,
  *                      and linear in the turns between them.

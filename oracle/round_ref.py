@@ -27,7 +27,7 @@ def rope_frequencies(rot, base, scaling="none", factor=1.0, original_len=0):
         for i, x in enumerate(f):
             w = min(max((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
             out.append(x * (1 - w) + x / factor * w)
-        return out, 0.1 * math.log(factor) + 1.0
+        return out, 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
     if scaling == "smooth":
         out = []
         for x in f:

@@ -68,6 +68,18 @@ def test_rope_plan(R, rot, scaling):
     assert not any(plan.c.turns[len(f):])
 
 
+@pytest.mark.parametrize("factor", [0.25, 0.5, 1.0, 1.5])
+def test_yarn_does_not_shrink(R, factor):
+    """Cosines and sines grow with the factor, and are left alone where it does not stretch."""
+    plan = R.Rope(64, 1e6, scaling="yarn", factor=factor, original_len=8192)
+    want = 0.1 * math.log(factor) + 1 if factor > 1 else 1.0
+    assert abs(plan.c.mscale - want) <= 2.0 ** -24 * want
+    f, m = ref.rope_frequencies(64, 1e6, "yarn", factor, 8192)
+    assert m == want
+    for i, x in enumerate(f):
+        assert abs(plan.c.turns[i] * 2 * math.pi - x) <= 1e-14 * x
+
+
 @pytest.mark.parametrize("args,status", [
     ((3, 1e4, 0, 0, 1.0, 0), ARG), ((0, 1e4, 0, 0, 1.0, 0), ARG), ((258, 1e4, 0, 0, 1.0, 0), UNSUP),
     ((64, 0.0, 0, 0, 1.0, 0), ARG), ((64, math.inf, 0, 0, 1.0, 0), ARG),

@@ -135,7 +135,7 @@ vqv_status vqv_rope_plan(vqv_rope* plan, int rot, double base, int interleaved, 
     };
     lo = fmax(floor(pair(32.0)), 0.0);
     hi = fmin(ceil(pair(1.0)), rot - 1.0);
-    plan->mscale = (float)(0.1 * log(factor) + 1.0);
+    if (factor > 1.0) plan->mscale = (float)(0.1 * log(factor) + 1.0);
   }
   for (int i = 0; i < 128; ++i) plan->turns[i] = 0.0;
   for (int i = 0; i < rot / 2; ++i) {
