@@ -343,6 +343,25 @@ def test_compact_bad_pages(vqv):
             [0, 1] * 6 + [0, 1, 1] * 4 + [1] * 6, bad=[(0, 3), (1, 2)])
 
 
+@pytest.mark.parametrize("kv", [-2 ** 31, -2 ** 31 + 2, -5, 2])
+def test_lengths_far_below_zero(vqv, kv):
+    """Rows before the first token are stored nowhere and move nowhere, also where their positions
+    pass 32 bits and the table is as wide; what stands on the pages that those would be on stays."""
+    ps, width = 1 << 20, 2048
+    cache = vqv.PagedCache(*(torch.full((1, 2, ps, 1, 64), x, dtype=torch.bfloat16, device="cuda") for x in (2.0, 3.0)))
+    seqs = vqv.Sequences(i32([0, 4]), i32([kv]), i32([[1] * width]), n_rows=4, max_rows=4, max_kv=4)
+    x = torch.randn(4, 1, 64, device="cuda")
+    q = vqv.vqv_rope_append(x, x, x, cache, seqs, vqv.Rope(2, interleaved=True))
+    out = vqv.vqv_paged_attn(q, cache, seqs, scale=1.0)
+    new = vqv.vqv_cache_compact(cache, seqs, i32([0, 1, 1, 0]))
+    assert new.tolist() == [max(kv - 2, -2 ** 31)]
+    first = max(kv, 0)                      # tokens that there are
+    assert (out[:4 - first] == 0).all() and (out[4 - first:] != 0).all()
+    for t, value in ((cache.k, 2.0), (cache.v, 3.0)):
+        assert (t[0, 0] == value).all() and (t[0, 1, first:] == value).all()
+        assert (t[0, 1, :first] != value).all()
+
+
 def test_round_in_a_graph(vqv):
     """Compact, trim and reserve replayed from a graph are as good as called."""
     ps, layers = 4, 2

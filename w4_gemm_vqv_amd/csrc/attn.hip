@@ -404,7 +404,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
   const int tiles = (pairs + ROWS - 1) / ROWS;
   if (n <= 0 || group >= (PAIRS ? (tiles + 1) / 2 : tiles)) return;
   const Tiles tile = tiles_of<PAIRS>(group, tiles);
-  const int pos0 = a.seqs.kv_len[b] - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
+  const int pos0 = max(a.seqs.kv_len[b], 0) - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
   const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
   const Blocks blocks =
       visible_blocks<BT>(pos0 + tile.first * ROWS / g,
@@ -741,7 +741,7 @@ __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a) {
   const int n = min(min(a.seqs.row_start[b + 1], a.seqs.n_rows) - row0, a.seqs.max_rows);
   if (r - row0 >= n) return;
   const int g = a.group, tiles = (n * g + ROWS - 1) / ROWS;
-  const int pos0 = a.seqs.kv_len[b] - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
+  const int pos0 = max(a.seqs.kv_len[b], 0) - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
   const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
   const Tiles tile =
       tiles_of<PAIRS>(group_of<PAIRS>(((r - row0) * g + head % g) / ROWS, tiles), tiles);

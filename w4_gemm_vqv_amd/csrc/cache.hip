@@ -372,8 +372,7 @@ __global__ __launch_bounds__(256) void cache_compact(const vqv_cache c, const vq
   const int b = blockIdx.y;
   const int first = max(s.row_start[b], 0), next = min(s.row_start[b + 1], s.n_rows);
   const int n = max(next - first, 0);
-  const int kv = s.kv_len[b];
-  const int p0 = kv - n;
+  const int64_t p0 = (int64_t)s.kv_len[b] - n;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 
   const int per = c.dim >> 3;
@@ -399,7 +398,8 @@ __global__ __launch_bounds__(256) void cache_compact(const vqv_cache c, const vq
       all += waves[w];
     }
     if (kept) {
-      const int t = p0 + i, d = p0 + done + rank;
+      // -1: before the first token
+      const int t = (int)max(p0 + i, (int64_t)-1), d = (int)max(p0 + done + rank, (int64_t)-1);
       const int tp = page_of(s, b, t, c.page_size, c.pages);
       const int dp = page_of(s, b, d, c.page_size, c.pages);
       const bool move = t != d && tp >= 0 && dp >= 0;
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(256) void cache_compact(const vqv_cache c, const vq
     }
     done += all;
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) new_len[b] = p0 + done;
+  if (blockIdx.x == 0 && threadIdx.x == 0) new_len[b] = (int)max(p0 + done, (int64_t)INT_MIN);
 }
 
 template <bool FORK>

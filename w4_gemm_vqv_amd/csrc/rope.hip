@@ -47,18 +47,19 @@ __device__ __forceinline__ void load8(const T* p, float* x) {
 
 template <typename TIN, typename TC>
 __global__ __launch_bounds__(kThreads) void rope_append(const RopeArgs a) {
-  __shared__ float cs[kMaxDim], sn[kMaxDim];  // per value of a head; (1, 0) past rot
+  __shared__ float cs[kMaxDim], sn[kMaxDim];  // of the first rot values of a head
   const int r = blockIdx.x;
   const int b = seq_of_row(a.seqs.row_start, a.seqs.n_seqs, r);
   if (b >= a.seqs.n_seqs) return;
   const int first = a.seqs.row_start[b], next = a.seqs.row_start[b + 1];
   if (r < first) return;
-  const int pos = a.seqs.kv_len[b] - (next - first) + (r - first);
+  const int64_t at_pos = (int64_t)a.seqs.kv_len[b] - (next - first) + (r - first);
+  const int pos = (int)(at_pos < -1 ? -1 : at_pos);  // of the cache: -1 is none
   const int D = a.cache.dim, rot = a.rope.rot, half = rot >> 1;
   const bool inter = a.rope.interleaved;
 
   for (int i = threadIdx.x; i < half; i += kThreads) {
-    const double turns = (double)pos * a.rope.turns[i];
+    const double turns = (double)at_pos * a.rope.turns[i];
     const float part = (float)(turns - rint(turns));
     float s, c;
     sincospif(2.0f * part, &s, &c);
