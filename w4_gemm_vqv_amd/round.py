@@ -17,6 +17,7 @@ import ctypes
 import torch
 
 from .vqv import VQV_BF16, VQV_FP16, VQV_FP32, VqvError
+from .vqv import _on_device
 from .vqv import lib as _load
 from .vqv import vqv_status_string, vqv_verify_workspace_bytes
 
@@ -281,8 +282,9 @@ def vqv_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache: Pa
     if q_out is None:
         q_out = _new((n, heads, cache.dim), cache.dtype, dev, stream)
     out = _take(q_out, "q_out", (n, heads, cache.dim), cache.dtype, dev)
-    _check(_round_lib().vqv_rope_append(*ins, _DTYPES[q.dtype], heads, cache.c, layer, seqs.c,
-                                        rope.c, out, _stream(stream, dev)))
+    _check(_on_device(
+        dev, _round_lib().vqv_rope_append, *ins, _DTYPES[q.dtype], heads, cache.c, layer, seqs.c,
+        rope.c, out, _stream(stream, dev)))
     return q_out
 
 
@@ -310,8 +312,9 @@ def vqv_paged_attn(q: torch.Tensor, cache: PagedCache, seqs: Sequences, scale: f
     need = 0 if workspace is not None else vqv_paged_attn_workspace_bytes(cache, seqs, heads,
                                                                           window, sinks)
     workspace, wp, wn = _scratch(workspace, need, dev, stream)
-    _check(_round_lib().vqv_paged_attn(qp, cache.c, layer, seqs.c, heads, scale, window, sinks, op,
-                                       wp, wn, _stream(stream, dev)))
+    _check(_on_device(
+        dev, _round_lib().vqv_paged_attn, qp, cache.c, layer, seqs.c, heads, scale, window, sinks,
+        op, wp, wn, _stream(stream, dev)))
     return out
 
 
@@ -326,9 +329,9 @@ def _list(t: torch.Tensor, name: str, n: int, device) -> int:
 def vqv_cache_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, stream=None) -> None:
     """Pages src[i] to dst[i] (int32), on all layers."""
     n = src.numel()
-    _check(_round_lib().vqv_cache_copy(cache.c, _list(src, "src", n, cache.device),
-                                       _list(dst, "dst", n, cache.device), n,
-                                       _stream(stream, cache.device)))
+    _check(_on_device(
+        cache.device, _round_lib().vqv_cache_copy, cache.c, _list(src, "src", n, cache.device),
+        _list(dst, "dst", n, cache.device), n, _stream(stream, cache.device)))
 
 
 def vqv_cache_trim(pages: Pages, keep_len: torch.Tensor, rows: torch.Tensor | None = None,
@@ -336,8 +339,9 @@ def vqv_cache_trim(pages: Pages, keep_len: torch.Tensor, rows: torch.Tensor | No
     """Gives back the pages of table rows (`rows`, or the first ones) past
     keep_len tokens."""
     n, dev = keep_len.numel(), pages.device
-    _check(_round_lib().vqv_cache_trim(pages.c, _list(keep_len, "keep_len", n, dev),
-                                       _list(rows, "rows", n, dev), n, _stream(stream, dev)))
+    _check(_on_device(
+        dev, _round_lib().vqv_cache_trim, pages.c, _list(keep_len, "keep_len", n, dev),
+        _list(rows, "rows", n, dev), n, _stream(stream, dev)))
 
 
 def vqv_cache_reserve(pages: Pages, goal_len: torch.Tensor, ok: torch.Tensor | None = None,
@@ -349,8 +353,9 @@ def vqv_cache_reserve(pages: Pages, goal_len: torch.Tensor, ok: torch.Tensor | N
         ok = _new(n, torch.int32, dev, stream)
     need = 0 if workspace is not None else vqv_cache_workspace_bytes(pages)
     workspace, wp, wn = _scratch(workspace, need, dev, stream)
-    _check(_round_lib().vqv_cache_reserve(pages.c, _list(goal_len, "goal_len", n, dev), n,
-                                          _list(ok, "ok", n, dev), wp, wn, _stream(stream, dev)))
+    _check(_on_device(
+        dev, _round_lib().vqv_cache_reserve, pages.c, _list(goal_len, "goal_len", n, dev), n,
+        _list(ok, "ok", n, dev), wp, wn, _stream(stream, dev)))
     return ok
 
 
@@ -365,9 +370,9 @@ def vqv_cache_fork(cache: PagedCache, pages: Pages, parent: torch.Tensor, child:
         ok = _new(n, torch.int32, dev, stream)
     need = 0 if workspace is not None else vqv_cache_workspace_bytes(pages)
     workspace, wp, wn = _scratch(workspace, need, dev, stream)
-    _check(_round_lib().vqv_cache_fork(cache.c, pages.c, _list(parent, "parent", n, dev),
-                                       _list(child, "child", n, dev), n, _list(ok, "ok", n, dev),
-                                       wp, wn, _stream(stream, dev)))
+    _check(_on_device(
+        dev, _round_lib().vqv_cache_fork, cache.c, pages.c, _list(parent, "parent", n, dev),
+        _list(child, "child", n, dev), n, _list(ok, "ok", n, dev), wp, wn, _stream(stream, dev)))
     return ok
 
 
@@ -379,9 +384,9 @@ def vqv_cache_compact(cache: PagedCache, seqs: Sequences, keep: torch.Tensor,
     _same(dev, seqs=seqs)
     if new_len is None:
         new_len = _new(seqs.n_seqs, torch.int32, dev, stream)
-    _check(_round_lib().vqv_cache_compact(cache.c, seqs.c, _list(keep, "keep", seqs.n_rows, dev),
-                                          _list(new_len, "new_len", seqs.n_seqs, dev),
-                                          _stream(stream, dev)))
+    _check(_on_device(
+        dev, _round_lib().vqv_cache_compact, cache.c, seqs.c, _list(keep, "keep", seqs.n_rows, dev),
+        _list(new_len, "new_len", seqs.n_seqs, dev), _stream(stream, dev)))
     return new_len
 
 
@@ -408,7 +413,8 @@ def vqv_logits_edit(logits: torch.Tensor, edits: Edits, draft: torch.Tensor | No
     if out is None:
         out = _new(logits.shape, torch.float32, dev, stream)
     op = _take(out, "out", (B * T, edits.vocab), torch.float32, dev)
-    _check(_round_lib().vqv_logits_edit(lp, edits.c, dp, T, mp, op, _stream(stream, dev)))
+    _check(_on_device(
+        dev, _round_lib().vqv_logits_edit, lp, edits.c, dp, T, mp, op, _stream(stream, dev)))
     return out
 
 
@@ -429,8 +435,9 @@ def vqv_logits_verify(logits: torch.Tensor, edits: Edits, draft: torch.Tensor | 
         margin = _new(B * T, torch.float32, dev, stream)
     need = 0 if workspace is not None else vqv_verify_workspace_bytes(B, T, edits.vocab)
     workspace, wp, wn = _scratch(workspace, need, dev, stream)
-    _check(_round_lib().vqv_logits_verify(
-        lp, edits.c, dp, _take(draft_len, "draft_len", (B,), torch.int32, dev), T, mp,
+    _check(_on_device(
+        dev, _round_lib().vqv_logits_verify, lp, edits.c, dp,
+        _take(draft_len, "draft_len", (B,), torch.int32, dev), T, mp,
         _take(argmax, "argmax", (B * T,), torch.int32, dev),
         _take(accept_len, "accept_len", (B,), torch.int32, dev),
         _take(margin, "margin", (B * T,), torch.float32, dev), wp, wn, _stream(stream, dev)))

@@ -84,9 +84,18 @@ def _check(status: int) -> None:
         raise VqvError(status, lib().vqv_status_string(status).decode())
 
 
-def _stream_handle(stream) -> int:
+def _on_device(device: torch.device, call, *args):
+    """call(*args) with the tensors' device as the current one, where the
+    library launches: a stream handle of 0 is that device's default stream."""
+    if device.index == torch._C._cuda_getDevice():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
+
+
+def _stream_handle(stream, device: torch.device) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        stream = torch.cuda.current_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -167,9 +176,10 @@ def vqv_qgemm(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor, biases: t
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws_ptr = _dev(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().vqv_qgemm(_dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"),
-                           _dev(biases, "biases"), _dev(y, "y"), M, K, N, group, act,
-                           ws_ptr, ws_bytes, _stream_handle(stream)))
+    _check(_on_device(
+        x.device, lib().vqv_qgemm, _dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"),
+        _dev(biases, "biases"), _dev(y, "y"), M, K, N, group, act, ws_ptr, ws_bytes,
+        _stream_handle(stream, x.device)))
     return y
 
 
@@ -206,10 +216,10 @@ def vqv_verify(logits: torch.Tensor, draft: torch.Tensor | None, B: int, T: int,
         workspace = torch.empty(max(vqv_verify_workspace_bytes(B, T, N), 16), dtype=torch.uint8,
                                 device=dev)
     dptr = _dev(draft, "draft") if (draft is not None and draft.numel()) else None
-    _check(lib().vqv_verify(_dev(logits, "logits"), dptr, B, T, N, _dev(argmax, "argmax"),
-                            _dev(accept_len, "accept_len"), _dev(workspace, "workspace"),
-                            workspace.numel() * workspace.element_size(),
-                            _stream_handle(stream)))
+    _check(_on_device(
+        dev, lib().vqv_verify, _dev(logits, "logits"), dptr, B, T, N, _dev(argmax, "argmax"),
+        _dev(accept_len, "accept_len"), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream, dev)))
     return argmax, accept_len
 
 
@@ -236,11 +246,10 @@ def vqv_verify_ex(logits: torch.Tensor, draft: torch.Tensor | None, B: int, T: i
     dptr = _dev(draft, "draft") if (draft is not None and draft.numel()) else None
     lptr = _dev(draft_len, "draft_len") if draft_len is not None else None
     mptr = _dev(margin, "margin") if margin is not None else None
-    _check(lib().vqv_verify_ex(_dev(logits, "logits"), dptr, lptr, B, T, N,
-                               _dev(argmax, "argmax"), _dev(accept_len, "accept_len"), mptr,
-                               _dev(workspace, "workspace"),
-                               workspace.numel() * workspace.element_size(),
-                               _stream_handle(stream)))
+    _check(_on_device(
+        dev, lib().vqv_verify_ex, _dev(logits, "logits"), dptr, lptr, B, T, N,
+        _dev(argmax, "argmax"), _dev(accept_len, "accept_len"), mptr, _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream, dev)))
     return argmax, accept_len, margin
 
 
@@ -277,12 +286,11 @@ def vqv_qgemm_verify(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
         need = vqv_qgemm_verify_workspace_bytes(M, K, N, group, act)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
     dptr = _dev(draft, "draft") if (draft is not None and draft.numel()) else None
-    _check(lib().vqv_qgemm_verify(_dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"),
-                                  _dev(biases, "biases"), _dev(y, "y") if y is not None else None,
-                                  M, K, N, group, act, dptr, B, T, _dev(argmax, "argmax"),
-                                  _dev(accept_len, "accept_len"), _dev(workspace, "workspace"),
-                                  workspace.numel() * workspace.element_size(),
-                                  _stream_handle(stream)))
+    _check(_on_device(
+        dev, lib().vqv_qgemm_verify, _dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"),
+        _dev(biases, "biases"), _dev(y, "y") if y is not None else None, M, K, N, group, act, dptr,
+        B, T, _dev(argmax, "argmax"), _dev(accept_len, "accept_len"), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _stream_handle(stream, dev)))
     return y, argmax, accept_len
 
 
@@ -321,12 +329,12 @@ def vqv_qgemm_verify_ex(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
     dptr = _dev(draft, "draft") if (draft is not None and draft.numel()) else None
     lptr = _dev(draft_len, "draft_len") if draft_len is not None else None
     mptr = _dev(margin, "margin") if margin is not None else None
-    _check(lib().vqv_qgemm_verify_ex(
-        _dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"), _dev(biases, "biases"),
-        _dev(y, "y") if y is not None else None, M, K, N, group, act, dptr, lptr, B, T,
-        _dev(argmax, "argmax"), _dev(accept_len, "accept_len"), mptr,
+    _check(_on_device(
+        dev, lib().vqv_qgemm_verify_ex, _dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"),
+        _dev(biases, "biases"), _dev(y, "y") if y is not None else None, M, K, N, group, act, dptr,
+        lptr, B, T, _dev(argmax, "argmax"), _dev(accept_len, "accept_len"), mptr,
         _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-        _stream_handle(stream)))
+        _stream_handle(stream, dev)))
     return y, argmax, accept_len, margin
 
 
@@ -360,10 +368,11 @@ def vqv_qgemm_verify_ex_noalloc(x: torch.Tensor, wq: torch.Tensor, scales: torch
     dptr = _dev(draft, "draft") if (draft is not None and draft.numel()) else None
     lptr = _dev(draft_len, "draft_len") if draft_len is not None else None
     mptr = _dev(margin, "margin") if margin is not None else None
-    _check(lib().vqv_qgemm_verify_ex_noalloc(
-        _dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"), _dev(biases, "biases"),
-        _dev(y, "y") if y is not None else None, M, K, N, group, act, dptr, lptr, B, T,
-        _dev(argmax, "argmax"), _dev(accept_len, "accept_len"), mptr, _stream_handle(stream)))
+    _check(_on_device(
+        dev, lib().vqv_qgemm_verify_ex_noalloc, _dev(x, "x"), _dev(wq, "wq"),
+        _dev(scales, "scales"), _dev(biases, "biases"), _dev(y, "y") if y is not None else None, M,
+        K, N, group, act, dptr, lptr, B, T, _dev(argmax, "argmax"), _dev(accept_len, "accept_len"),
+        mptr, _stream_handle(stream, dev)))
     return y, argmax, accept_len, margin
 
 
@@ -393,7 +402,8 @@ def vqv_qgemm_swiglu(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     ws_ptr = _dev(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib().vqv_qgemm_swiglu(_dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"),
-                                  _dev(biases, "biases"), _dev(h, "h"), M, K, N, group, act,
-                                  ws_ptr, ws_bytes, _stream_handle(stream)))
+    _check(_on_device(
+        x.device, lib().vqv_qgemm_swiglu, _dev(x, "x"), _dev(wq, "wq"), _dev(scales, "scales"),
+        _dev(biases, "biases"), _dev(h, "h"), M, K, N, group, act, ws_ptr, ws_bytes,
+        _stream_handle(stream, x.device)))
     return h
