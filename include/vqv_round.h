@@ -224,6 +224,13 @@ vqv_status vqv_cache_fork(const vqv_cache* cache, const vqv_pages* pages, const 
  * layers, k and v. new_len[b] (int32) = kv_len[b] - rows + kept rows. What is
  * in the places behind stays as it was. A row on a bad page is not moved, and
  * a place on a bad page is not written.
+ *   The bytes move as they are. A prefix of the rows, which is what a greedy
+ * verify confirms, moves nothing: the call then only forms new_len. A row that
+ * is kept behind one that is not keeps the key that was turned for its old
+ * place (vqv_rope_append gives row i position kv_len - n + i), and its values
+ * are of a block in which it saw the dropped rows (vqv_paged_attn is causal by
+ * row order). Such a row is right only where neither matters; else feed it
+ * again.
  */
 vqv_status vqv_cache_compact(const vqv_cache* cache, const vqv_seqs* seqs, const int32_t* keep,
                              int32_t* new_len, void* hip_stream);

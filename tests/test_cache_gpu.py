@@ -336,6 +336,24 @@ def test_compact_many_rows(vqv):
     compact(vqv, SHAPES[0], rows, [605, 400], [i % 2 for i in range(sum(rows))])
 
 
+def test_compact_moves_bytes(vqv):
+    """A prefix stays, bit for bit; a key kept behind a dropped row is still turned for its old place."""
+    x = torch.randn(5, 1, 64, generator=torch.Generator().manual_seed(4)).cuda()
+    rope = vqv.Rope(64)
+    seqs = vqv.Sequences(i32([0, 5]), i32([9]), i32([[2, 0, 1]]), n_rows=5, max_rows=5, max_kv=9)
+    cache = pair(vqv, (1, 4, 1, 64, torch.bfloat16, "slot"), 3)
+    vqv.vqv_rope_append(x, x, x, cache, seqs, rope)
+    before = [bits(cache.k), bits(cache.v)]
+    assert vqv.vqv_cache_compact(cache, seqs, i32([1, 1, 1, 0, 0])).tolist() == [7]
+    assert torch.equal(bits(cache.k), before[0]) and torch.equal(bits(cache.v), before[1])
+    assert vqv.vqv_cache_compact(cache, seqs, i32([1, 0, 0, 1, 0])).tolist() == [6]
+    f, m = ref.rope_frequencies(64, 10000.0)
+    got = cache.k[0, 0, 1].double().cpu()          # token 5: row 3 of positions 4..8
+    old, new = (ref.rope_ref(x[3].cpu(), p, f, m, 64, False) for p in (7, 5))
+    assert ((got - old).abs() <= 2.0 ** -8 * old.abs() + 1e-5).all() and (got - new).abs().max() > 0.1
+    assert torch.equal(cache.v[0, 0, 1], x[3].to(torch.bfloat16))
+
+
 def test_compact_bad_pages(vqv):
     """A row on a page that is none is not moved, nor is one whose place is on
     such a page; rows before the first token neither."""

@@ -337,7 +337,8 @@ def vqv_cache_copy(cache: PagedCache, src: torch.Tensor, dst: torch.Tensor, stre
 def vqv_cache_trim(pages: Pages, keep_len: torch.Tensor, rows: torch.Tensor | None = None,
                    stream=None) -> None:
     """Gives back the pages of table rows (`rows`, or the first ones) past
-    keep_len tokens."""
+    keep_len tokens. A row that is cut inside pages that others hold too gets
+    no room from vqv_cache_reserve: go on with a fork of it."""
     n, dev = keep_len.numel(), pages.device
     _check(_on_device(
         dev, _round_lib().vqv_cache_trim, pages.c, _list(keep_len, "keep_len", n, dev),
@@ -347,7 +348,8 @@ def vqv_cache_trim(pages: Pages, keep_len: torch.Tensor, rows: torch.Tensor | No
 def vqv_cache_reserve(pages: Pages, goal_len: torch.Tensor, ok: torch.Tensor | None = None,
                       workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Takes free pages until the first rows hold goal_len tokens' worth;
-    returns ok [rows] int32."""
+    returns ok [rows] int32, 0 where there are too few or the row's next token
+    would be written to a page that other rows hold too."""
     n, dev = goal_len.numel(), pages.device
     if ok is None:
         ok = _new(n, torch.int32, dev, stream)
@@ -379,7 +381,9 @@ def vqv_cache_fork(cache: PagedCache, pages: Pages, parent: torch.Tensor, child:
 def vqv_cache_compact(cache: PagedCache, seqs: Sequences, keep: torch.Tensor,
                       new_len: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Moves each sequence's kept rows (keep [n_rows] int32, not 0) together,
-    on all layers; returns its new lengths [n_seqs] int32."""
+    on all layers; returns its new lengths [n_seqs] int32. The bytes move as
+    they are: a prefix of the rows stays where it is, a row kept behind a
+    dropped one keeps a key that was turned for its old place."""
     dev = cache.device
     _same(dev, seqs=seqs)
     if new_len is None:
