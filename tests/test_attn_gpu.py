@@ -266,13 +266,13 @@ def test_refuses_wrong_tensors(vqv):
         vqv.vqv_paged_attn(c.qd, c.cache, c.seqs, scale=0.0)
 
 
-def near(c, got, want, low=0.0):
-    """As `close`, for scores of one product each, where the largest weight of a wave's tokens is 1
+def near(c, got, want, low=0.0, terms=1):
+    """As `close`, for scores of `terms` products each, where the largest weight of a wave's tokens is 1
     exactly (`want`'s mean is then what the others come to) and fp16 weights are 2^15 times as
     large: off by up to 2^-25 of that where they are subnormal; low is the sum of |v| over tokens."""
     out, mean, size = want
     half, n = torch.finfo(c.t).eps / 2, max(c.kv)
-    score = size * 9 * 2.0 ** -24 + 2.0 ** -22
+    score = size * (terms + 8) * 2.0 ** -24 + 2.0 ** -22
     inner = (2 * score + (n + 8) * 2.0 ** -24) * torch.maximum(mean, out.abs()) + half * mean
     if c.t == torch.float16:
         inner = inner + 2.0 ** -40 * low
@@ -381,3 +381,41 @@ def test_no_rows(vqv):
     assert vqv.vqv_cache_compact(c.cache, seqs, i32([])).tolist() == [20, 7]
     for x, y in zip((c.cache.k, c.cache.v), before):
         assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+
+
+# Rows of a case (two heads to a key head) that take 32, 64, 128 and, up to dim 128 without a
+# window, two tiles of 128 (row, head) pairs of a work-group.
+ROWS = [3, 20, 50, 90]
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 5)])
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 80, 96, 128, 192, 256])
+def test_many_blocks_of_one_work_group(vqv, dim, dtype, rows, window, sinks):
+    """A max_kv that plans one split: every work-group walks over 10 blocks and more, past what it
+    looks up ahead; odd pages, some of them none, NaN in every slot without a token."""
+    c = Case(rows=[rows, 2], kv=[1501, 1290], heads=4, hk=2, dim=dim, ps=20, dtype=dtype,
+             layout="head" if dim % 64 else "slot", seed=dim + rows, max_kv=64)
+    c.table[0][70], c.table[0][31], c.table[1][50], c.table[1][3] = -1, c.pages, 1 << 30, -7
+    near(c, c.run(vqv, window, sinks), c.want(window, sinks), 5.0 * 1501, dim)
+
+
+@pytest.mark.parametrize("rows", ROWS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("dim", [64, 128, 192, 256])
+def test_maximum_jumps_between_blocks(vqv, dim, dtype, rows):
+    """The maximum passes the one before it by far, block after block, up and then down: what was
+    summed is scaled to nothing or kept as it is."""
+    for sign in (1, -1):
+        steps = [(i * 71, sign * 12.0 * i) for i in range(1, 18)]
+        c = ladder(rows, dim, dtype, steps, seed=rows)
+        near(c, c.run(vqv, scale=1.0), c.want(scale=1.0))
+
+
+@pytest.mark.parametrize("rows,dim,dtype", [(1, 128, "bf16"), (8, 256, "fp16"), (200, 64, "bf16"), (130, 128, "fp16")])
+def test_long_sequences(vqv, rows, dim, dtype):
+    """Tens of thousands of tokens in many splits, the last one short."""
+    c = Case(rows=[rows], kv=[24001], heads=2, hk=1, dim=dim, ps=64, dtype=dtype, seed=rows)
+    near(c, c.run(vqv), c.want(), 5.0 * 24001, dim)
+    near(c, c.run(vqv, 9000, 100), c.want(9000, 100), 5.0 * 24001, dim)
