@@ -137,10 +137,13 @@ vqv_status vqv_rope_append(const void* q, int64_t q_row_stride, int64_t q_head_s
  *   dim        64, 80, 96, 128, 192 or 256 (else VQV_ERR_UNSUPPORTED).
  *   workspace  vqv_paged_attn_workspace_bytes bytes, 16-byte aligned; may be
  *              NULL when that is 0. Its contents on entry do not matter.
- * Scores, maxima, sums and the output are held in fp32; the weights p_j,
- * relative to the largest so far, are rounded to the cache's type (half a step
- * each, the largest is exact; in fp16 those 2^29 below the largest by up to
- * 2^-40 of it) for the product with v and for their sum.
+ * Scores, maxima, sums and the output are held in fp32. For the product with v
+ * the weights p_j, relative to the largest so far, are held in two values of
+ * the cache's type (to 2^-16 of a weight in bf16, 2^-22 in fp16) where max_rows
+ * rows of a key head's queries are 64 or fewer, as in decoding and verify
+ * blocks; for longer chunks they are rounded to one (half a step each, the
+ * largest is exact). fp16 weights 2^29 below the largest are off by up to 2^-39
+ * of it.
  */
 size_t vqv_paged_attn_workspace_bytes(const vqv_cache* cache, const vqv_seqs* seqs, int heads,
                                       int window, int sinks);

@@ -419,3 +419,37 @@ def test_long_sequences(vqv, rows, dim, dtype):
     c = Case(rows=[rows], kv=[24001], heads=2, hk=1, dim=dim, ps=64, dtype=dtype, seed=rows)
     near(c, c.run(vqv), c.want(), 5.0 * 24001, dim)
     near(c, c.run(vqv, 9000, 100), c.want(9000, 100), 5.0 * 24001, dim)
+
+
+@pytest.mark.parametrize("rows,dim", [(1, 64), (3, 80), (8, 128), (16, 96), (30, 128), (25, 192), (16, 256), (32, 256)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_few_rows_are_as_good_as_fp32(vqv, rows, dim, dtype):
+    """Up to 64 (row, head) pairs the weights are held to 2^-16 (bf16) or 2^-22, twice the type's
+    bits: beside the output's own rounding an error of that and of fp32 sums."""
+    c = Case(rows=[rows, 1], kv=[700, 333], heads=2, hk=1, dim=dim, ps=16, dtype=dtype, seed=rows)
+    for window, sinks in ((0, 0), (200, 3)):
+        got, (out, mean, size) = c.run(vqv, window, sinks), c.want(window, sinks)
+        half = torch.finfo(c.t).eps / 2
+        score = size * (dim + 8) * 2.0 ** -24 + 2.0 ** -22
+        inner = (half ** 2 + 2 * score + (700 + 8) * 2.0 ** -24) * mean
+        if dtype == "fp16":
+            inner = inner + 2.0 ** -40 * 5.0 * 700
+        allow = half * (out.abs() + inner) + inner + 2.0 ** -25
+        err = (got.double() - out).abs()
+        assert (err <= allow).all(), f"error over allowance {(err / allow).max():.3g}"
+
+
+@pytest.mark.parametrize("rows,dim", SHAPES_OF_WAVES)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_infinity_behind_a_small_weight(vqv, rows, dim, dtype):
+    """Weights that are powers of two (nothing is left over by their rounding): an infinity among
+    the values comes out as one, not as NaN."""
+    c = ladder(rows, dim, dtype, [(0, 0.0), (512, 0.0)])
+    c.q[:, :, 0] = 1.0
+    for depth in (0, 1, 7, 20, 30, 38):
+        c.k[0, c.table[0][32], 0, :, 0] = -depth
+        for x in (float("inf"), -float("inf")):
+            c.v[0, c.table[0][32], 0, :, 11] = x
+            got = c.run(vqv, scale=0.6931471805599453)
+            assert (got[:, :, 11] == x).all(), depth
+            assert got.isfinite().sum() == got.numel() - got[:, :, 11].numel()

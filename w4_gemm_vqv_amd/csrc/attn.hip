@@ -30,11 +30,18 @@
 // needs no exchange at all.
 //
 // Softmax runs with base-2 exponentials and a running maximum; scores, maxima,
-// sums and outputs are fp32. P is rounded to the cache's type, the matrix instruction's
-// input: an error of at most half a step of each weight, none of the largest,
-// which the sum over tokens averages. The largest is 1, in fp16 2^15 (the sum
-// of weights is as much larger): with 1 a token 2^14 below it would lose bits,
-// and thousands of them 2^25 below would be nothing.
+// sums and outputs are fp32. P goes to the matrix instruction in the cache's
+// type. Up to 64 (row, head) pairs, where memory bounds the kernel, it goes
+// twice, cut to its bits and what that left over (to 2^-16 of a weight in bf16,
+// 2^-22 in fp16): the outputs are then the fp32 form's but for the order of
+// sums (decoding 349 us, rounded once 350; a block of 8 rows 15.6 and 15.2; 16
+// blocks of 16 rows, dim 256, 78 and 76). Beyond that it is rounded once, an
+// error of at most half a step of each weight, none of the largest, which the
+// sum over tokens averages: a second product would take 478 us of a prompt
+// chunk for 369, for an error of 1.66e-3 instead of 2.15e-3 (of which the
+// output's own rounding is 1.66e-3). The largest weight is 1, in fp16 2^15 (the
+// sum of weights is as much larger): with 1 a token 2^14 below it would lose
+// bits, and thousands of them 2^25 below would be nothing.
 
 #include <limits.h>
 
@@ -120,6 +127,27 @@ __device__ __forceinline__ float add2<_Float16>(unsigned w, float c) {
   typedef __attribute__((ext_vector_type(2))) _Float16 t2;
   return __builtin_amdgcn_fdot2(__builtin_bit_cast(t2, w),
                                 t2{(_Float16)1.0f, (_Float16)1.0f}, c, false);
+}
+
+// a and b (0 or more), cut to T, and what that leaves. The rest is never 0
+// unless the weight is, so that the product of both with an infinity is one.
+template <typename T>
+__device__ __forceinline__ u32x2 split2(float a, float b);
+template <>
+__device__ __forceinline__ u32x2 split2<__bf16>(float a, float b) {
+  constexpr float up = 1.0f + 0x1p-22f;
+  const unsigned x = __float_as_uint(a), y = __float_as_uint(b);
+  return u32x2{__builtin_amdgcn_perm(y, x, 0x07060302u),
+               pack2<__bf16>(fmaf(a, up, -__uint_as_float(x & 0xFFFF0000u)),
+                             fmaf(b, up, -__uint_as_float(y & 0xFFFF0000u)))};
+}
+template <>
+__device__ __forceinline__ u32x2 split2<_Float16>(float a, float b) {
+  constexpr float least = 0x1p-24f;
+  const auto r = __builtin_amdgcn_cvt_pkrtz(a, b);
+  return u32x2{__builtin_bit_cast(unsigned, r),
+               pack2<_Float16>(__builtin_amdgcn_fmed3f(a - (float)r[0], least, a),
+                               __builtin_amdgcn_fmed3f(b - (float)r[1], least, b))};
 }
 
 // Not 0 where one of two packed values is an infinity or NaN: an exponent of
@@ -294,13 +322,18 @@ __device__ __forceinline__ s16x8 values(unsigned at, int u, int d) {
 // A block whose values hold infinities or NaN, some rows not seeing all of its
 // tokens. A function of its own: it seldom runs, and takes no registers from
 // the loop. `seen` are the bits of the tokens that the lane's row sees.
+// Weights of 16 tokens in one value each of the cache's type, or in two.
+struct Weights {
+  s16x8 high, low;
+};
+
 template <int DB, int SUB>
 struct BadBlock {
   f32x16 o[DB];
-  s16x8 weights[2 * SUB];
+  Weights weights[2 * SUB];
 };
 
-template <typename T, int D, int SUB>
+template <typename T, int D, int SUB, bool FINE>
 __device__ __attribute__((noinline)) void product_with_bad_values(
     BadBlock<(D + 31) / 32, SUB>& x, unsigned seen, unsigned vs) {
   vs += value_address<D>(threadIdx.x & 63);
@@ -309,8 +342,11 @@ __device__ __attribute__((noinline)) void product_with_bad_values(
     f32x16 o = x.o[d];
     add_not_finite<T, 2 * SUB>([&](int u) { return values<D>(vs, u, d); }, seen, o);
 #pragma unroll
-    for (int u = 0; u < 2 * SUB; ++u)
-      o = mfma<T>(finite<T>(values<D>(vs, u, d)), x.weights[u], o);
+    for (int u = 0; u < 2 * SUB; ++u) {
+      const s16x8 v = finite<T>(values<D>(vs, u, d));
+      o = mfma<T>(v, x.weights[u].high, o);
+      if (FINE) o = mfma<T>(v, x.weights[u].low, o);
+    }
     x.o[d] = o;
   }
 }
@@ -373,6 +409,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
     const AttnArgs a) {
   constexpr int NW = MW * KW, BT = KW * KT, DC = D / 8, DS = D / 16, DB = (D + 31) / 32;
   constexpr bool PAIRS = MW == 8;
+  constexpr bool FINE = MW <= 2;
   constexpr int ROWS = PAIRS ? 128 : 32 * MW;        // (row, head) pairs of a tile
   constexpr int GROUPS = BT * DC / 64;               // of 64 pieces: a wave's access
   constexpr int LOADS = (GROUPS + NW - 1) / NW;      // per wave, of keys and of values
@@ -604,10 +641,11 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[u][i] -= base;
     }
-    // The weights of 16 tokens, as the B operand of their product. The sum
-    // takes them as rounded, as the product does.
+    // The weights of 16 tokens, as the B operand of their product. FINE: in
+    // two values each. Else the sum takes them as rounded, as the
+    // product does.
     const auto weights = [&](int u) {
-      u32x4 w;
+      u32x4 high, low = {};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float p[2];
@@ -615,10 +653,18 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
         for (int e = 0; e < 2; ++e)
           p[e] = __builtin_amdgcn_exp2f(
               fmaf(s[u / 2][8 * (u & 1) + 2 * i + e], a.scale_log2, -shift));
-        w[i] = pack2<T>(p[0], p[1]);
-        sum = add2<T>(w[i], sum);
+        if (FINE) {
+          const u32x2 w = split2<T>(p[0], p[1]);
+          high[i] = w[0];
+          low[i] = w[1];
+          sum += p[0] + p[1];
+        } else {
+          const unsigned w = pack2<T>(p[0], p[1]);
+          high[i] = w;
+          sum = add2<T>(w, sum);
+        }
       }
-      return __builtin_bit_cast(s16x8, w);
+      return Weights{__builtin_bit_cast(s16x8, high), __builtin_bit_cast(s16x8, low)};
     };
 
     // A hidden token's weight is 0, which an infinity or NaN of its values
@@ -640,17 +686,21 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
       for (int u = 0; u < 2 * SUB; ++u) x.weights[u] = weights(u);
 #pragma unroll
       for (int d = 0; d < DB; ++d) x.o[d] = o[d];
-      product_with_bad_values<T, D, SUB>(x, seen, lds_offset(vs));
+      product_with_bad_values<T, D, SUB, FINE>(x, seen, lds_offset(vs));
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[d] = x.o[d];
     } else {
       // The next 16 tokens' weights are formed while the matrix unit works.
-      s16x8 next = weights(0);
+      Weights next = weights(0);
 #pragma unroll
       for (int u = 0; u < 2 * SUB; ++u) {
-        const s16x8 pf = next;
+        const Weights p = next;
 #pragma unroll
-        for (int d = 0; d < DB; ++d) o[d] = mfma<T>(values<D>(va, u, d), pf, o[d]);
+        for (int d = 0; d < DB; ++d) {
+          const s16x8 v = values<D>(va, u, d);
+          o[d] = mfma<T>(v, p.high, o[d]);
+          if (FINE) o[d] = mfma<T>(v, p.low, o[d]);
+        }
         if (u + 1 < 2 * SUB) next = weights(u + 1);
       }
     }
