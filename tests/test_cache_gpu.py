@@ -267,6 +267,44 @@ def test_fork_refused_pairs(vqv):
     dev.check(book)
 
 
+def test_copy_many_pairs(vqv):
+    """More pairs than a launch's second dimension holds."""
+    n = 70001
+    cache = pair(vqv, (1, 1, 1, 8, torch.bfloat16, "slot"), 2 * n)
+    order = torch.randperm(2 * n, generator=torch.Generator().manual_seed(2))
+    want = [bits(x) for x in (cache.k, cache.v)]
+    for x in want:
+        x[:, order[n:]] = x[:, order[:n]]
+    vqv.vqv_cache_copy(cache, order[:n].to(torch.int32).cuda(), order[n:].to(torch.int32).cuda())
+    torch.cuda.synchronize()
+    for got, w in zip((cache.k, cache.v), want):
+        assert torch.equal(bits(got), w)
+
+
+@pytest.mark.parametrize("n", [1025, 70000])
+def test_fork_many_pairs(vqv, n):
+    """More branches than the book's work-group has threads, and than a launch holds; one page too few."""
+    pages, ps = n + 2, 2
+    cache = pair(vqv, (1, ps, 1, 8, torch.bfloat16, "slot"), pages)
+    table = torch.full((n + 1, 2), -1, dtype=torch.int32, device="cuda")
+    table[0] = i32([5, 2])
+    refs, held, length = (torch.zeros(m, dtype=torch.int32, device="cuda") for m in (pages, n + 1, n + 1))
+    refs[[5, 2, 9]] = 1                       # page 9 is another's
+    held[0], length[0] = 2, 3
+    book = vqv.Pages(refs, table, held, length, page_size=ps)
+    child = torch.arange(1, n + 1, dtype=torch.int32, device="cuda")
+    ok = vqv.vqv_cache_fork(cache, book, torch.zeros_like(child), child)
+    free = torch.tensor([p for p in range(pages) if p not in (5, 2, 9)], dtype=torch.int32, device="cuda")
+    good = free.numel()
+    assert good == n - 1 and ok[:good].all() and ok[good] == 0
+    assert (table[1:n, 0] == 5).all() and torch.equal(table[1:n, 1], free) and (table[n] == -1).all()
+    assert refs[5] == n and (refs[free.long()] == 1).all() and refs[2] == refs[9] == 1
+    assert (held[1:n] == 2).all() and (length[1:n] == 3).all() and held[n] == length[n] == 0
+    for x in (cache.k, cache.v):
+        x = x.view(torch.int16)
+        assert (x[0, free.long()] == x[0, 2]).all()
+
+
 @pytest.mark.parametrize("bad", [-1, 6, 1 << 30])
 def test_fork_bad_pages(vqv, bad):
     """A parent whose last page is none has no branch (its tokens there are hidden; a new page

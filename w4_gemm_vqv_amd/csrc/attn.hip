@@ -10,9 +10,9 @@
 // split over work-groups, whose partial sums a second kernel joins. With many,
 // eight waves share a block's loads: two tiles of 128 rows, one from the
 // chunk's beginning and one from its end, so that all work-groups have as much
-// to do (2048 rows of 32 heads over 10240 tokens: 379 us, with one tile per
-// work-group 405). Under a window the two would not see the same tokens: one
-// tile (3 chunks of up to 1500 rows, window 1023: 73 us, with two 78).
+// to do (2048 rows of 32 heads over 10240 tokens: 369 us, with four waves and one
+// tile 393). Under a window the two would not see the same tokens: one tile (3
+// chunks of up to 1500 rows, window 1023: 75 us, with two tiles 105).
 //
 // Loads go to LDS without registers between, up to STAGES - 1 blocks ahead. A
 // block's places in the cache are found before that: its entries of the page
@@ -245,7 +245,7 @@ __device__ __forceinline__ void staged() {
 
 // The order of a run of N matrix instructions that each take an LDS read: the
 // reads of AHEAD of them go first, and then one's with each (left to itself the
-// compiler waits for each read in turn: a prompt chunk took 709 us, not 439).
+// compiler waits for more of them in turn: a prompt chunk takes 388 us, not 369).
 template <int N, int AHEAD>
 __device__ __forceinline__ void pipelined() {
   constexpr int ahead = N < AHEAD ? N : AHEAD;
@@ -906,10 +906,10 @@ AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window,
   // Blocks of a split. Full tiles: as many work-groups as fit the 256 CUs at
   // once, splits of 4 blocks at least. Few query rows: one work-group per
   // CU while that leaves splits of 16 blocks or fewer (a block of 8 rows over
-  // 4096 tokens: 14.6 us, with two per CU 16.3, one for two CUs 16.7); then
+  // 4096 tokens: 15.8 us, with two per CU 17.2, one for two CUs 18.6); then
   // splits of 16 or more, in 16 rounds as lengths differ (48 ragged sequences:
-  // 376 us, in 8 rounds 403, in 4 455), but in two where a window makes them
-  // alike (74 us, in 4 rounds 82).
+  // 350 us, in 8 rounds 361, in 4 407), but in two where a window makes them
+  // alike (80 us, in 4 rounds 84).
   int64_t per;
   if (p.mw >= 4) {
     per = ceil_div(blocks * base, p.mw == 4 && c.dim <= 128 ? 512 : 256);
