@@ -6,9 +6,9 @@
 // whole GPU in 16-byte pieces; they are bound by memory. Sums of references
 // are integer atomics, so their order does not matter, and free pages are
 // given out by rank (prefix sums), so the result does not depend on timing. The
-// end of a round of 32 blocks of 16 rows, 16 layers and 6000 pages takes 14.6
-// us: compact 5.5, trim 2.6, reserve 6.9, each bound by the latency of the few
-// loads that follow one another.
+// end of a round of 32 blocks of 16 rows, 16 layers and 6000 pages takes 15 to
+// 16 us: compact 5.4, trim 2.8, reserve 7.2, each bound by the latency of the
+// few loads that follow one another.
 
 #include <limits.h>
 
@@ -158,7 +158,7 @@ __device__ __forceinline__ bool ends_in_shared_page(const vqv_pages& pg, int i, 
 // One work-group. off[]: the rank of each row's first new page, in LDS while
 // the rows fit there. Loads that do not depend on each other go out together,
 // and what a thread has read it keeps, as their latency is all the time there
-// is (32 rows and 6000 pages: 8.5 us before, 6.9 so; the look at each row's last
+// is (32 rows and 6000 pages: 8.5 us before, 7.2 so; the look at each row's last
 // page does not show in the end of a round, 15.1 us with and without).
 __global__ __launch_bounds__(kBook) void cache_reserve(const vqv_pages pg,
                                                        const int32_t* __restrict__ goal_len,

@@ -14,8 +14,8 @@
 //
 // The floor is memory: logits once (and once out), counts once per sequence.
 // 64 rows over 151936 tokens with all edits and the verify take 30 us, 8.8 of
-// them the floor: 53 vector instructions per token and row keep the vector
-// units busy 40 % of the time, and the loads that follow one another at a
+// them the floor: 39 vector instructions per token and row keep the vector
+// units busy 35 % of the time, and the loads that follow one another at a
 // work-group's start (biases, counts, the first row) take most of the rest.
 
 #include "argmax.h"
