@@ -1,25 +1,9 @@
 // Entry points of include/vqv_round.h: argument checks on the host, then the
 // launches on the caller's stream.
 
-#include <math.h>
-#include <stdint.h>
-
-#include "round_internal.h"
+#include "api_checks.h"
 
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Whether every non-NULL pointer of the list can hold int32 or fp32 values.
-template <typename... P>
-bool words_aligned(const P*... p) {
-  return (... && aligned(p, 4));
-}
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a && b && na && nb && a0 < b0 + nb && b0 < a0 + na;
-}
 
 vqv_status check_cache(const vqv_cache* c) {
   if (!c || !c->k || !c->v) return VQV_ERR_ARG;
@@ -42,16 +26,6 @@ vqv_status check_cache(const vqv_cache* c) {
   if ((int64_t)c->page_size * c->kv_heads * (c->dim / 8) >= (1ll << 31) ||
       (int64_t)c->layers * 2 * c->kv_heads * (c->dim / 8) >= (1ll << 31))
     return VQV_ERR_UNSUPPORTED;
-  return VQV_OK;
-}
-
-vqv_status check_seqs(const vqv_seqs* s) {
-  if (!s || !s->row_start || !s->kv_len || !s->table) return VQV_ERR_ARG;
-  if (s->n_seqs < 1 || s->table_width < 1 || s->n_rows < 0 || s->max_rows < 0 || s->max_kv < 0 ||
-      s->table_stride < s->table_width)
-    return VQV_ERR_ARG;
-  if (s->n_seqs > 65535) return VQV_ERR_UNSUPPORTED;
-  if (!words_aligned(s->row_start, s->kv_len, s->table)) return VQV_ERR_ALIGN;
   return VQV_OK;
 }
 
@@ -104,8 +78,6 @@ bool any_overlap(const void* p, size_t n, const EditSpans& s) {
     if (overlaps(p, n, x.p, x.n)) return true;
   return false;
 }
-
-vqv_status status_of(hipError_t e) { return e == hipSuccess ? VQV_OK : VQV_ERR_HIP; }
 
 }  // namespace
 
@@ -179,7 +151,7 @@ vqv_status vqv_rope_append(const void* q, int64_t q_row_stride, int64_t q_head_s
     return VQV_ERR_UNSUPPORTED;
   if (seqs->n_rows == 0) return VQV_OK;
   const auto span = [&](int64_t rs, int64_t hs, int h) {
-    return (size_t)((seqs->n_rows - 1) * rs + (h - 1) * hs + cache->dim) * esz;
+    return rows_span(seqs->n_rows, rs, hs, h, cache->dim, esz);
   };
   const size_t out = (size_t)seqs->n_rows * heads * cache->dim * 2;
   if (overlaps(q_out, out, q, span(q_row_stride, q_head_stride, heads)) ||
