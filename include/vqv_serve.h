@@ -86,12 +86,14 @@ vqv_status vqv_cache_q4_read(const vqv_cache_q4* cache, int layer, const vqv_seq
  * vqv_paged_attn over a 4-bit cache: arguments and formula as there, k_j and
  * v_j being the records' values, and
  *   dtype      type of q and out, VQV_BF16 or VQV_FP16.
- * Scores, maxima, sums and the output are held in fp32. Keys and values enter
- * the matrix products in fp16, rounded once from scale * code + bias (2^-12 of
- * a value; values are to stay below 65504), bf16 queries in fp16 times a power
- * of two per row (a query value 2^24 below its row's largest loses bits). The
- * weights p_j as in vqv_paged_attn with an fp16 cache: in two values where
- * max_rows rows of a key head's queries are 64 or fewer, else rounded once.
+ * Scores, maxima, sums and the output are held in fp32. The matrix products
+ * take fp16: values rounded once from scale * code + bias (2^-12 of a value; they
+ * are to stay below 65504), keys so for bf16 queries and in two such numbers (to
+ * 2^-22) for fp16 ones, bf16 queries times a power of two per row (a query value
+ * 2^24 below its row's largest loses bits). The weights p_j, relative to the
+ * largest so far, are rounded once too; for fp16 outputs they are two numbers
+ * (to 2^-22) where max_rows rows of a key head's queries are 64 or fewer.
+ * Weights 2^29 below the largest are off by up to 2^-39 of it.
  */
 size_t vqv_paged_attn_q4_workspace_bytes(const vqv_cache_q4* cache, const vqv_seqs* seqs,
                                          int heads, int window, int sinks);

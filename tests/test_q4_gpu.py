@@ -238,25 +238,27 @@ class Case:
         return out.cpu()
 
     def want(self, window=0, sinks=0, scale=None, rounded=True):
-        """In 64 bits, over the values as they enter the products (one rounding to fp16), or exact ones."""
+        """In 64 bits, over the values as they enter the products (one rounding to fp16, but for the
+        keys of fp16 queries, which enter in two values), or exact ones."""
         k, v = (q4.unpack(x[self.layer], self.dim) for x in (self.rk, self.rv))
         if rounded:
-            k, v = k.half().double(), v.half().double()
+            k, v = k.half().double() if self.t == torch.bfloat16 else k, v.half().double()
         return ref.attn_ref(self.q, k, v, self.start, self.kv, self.table, scale or self.scale, window, sinks)
 
     def allowance(self, want, values=0.0, low=0.0, terms=None):
         """Half a step of the output, after: a score's error, which moves its weight by as much,
         relatively (`terms` products and sums in fp32 of sizes up to `size`, one scaling, one
-        subtraction, an exponential of 2^-22), for the weight and for the sum of weights; a bf16
-        query 2^24 below its row's largest is off by up to 2^-35 of that; weights in two fp16
-        values (2^-22) up to 64 pairs, else in one (2^-11); below 2^-29 of the largest they are
+        subtraction, an exponential of 2^-22), for the weight and for the sum of weights; keys in two
+        values (2^-22) of fp16 queries; a bf16 query 2^24 below its row's largest is off by up to 2^-35 of that; weights in two fp16
+        values (2^-22) for fp16 outputs of up to 64 pairs, else in one (2^-11); below 2^-29 of the largest they are
         off by 2^-40 of it, of which `low` is the sum of |v|; sums over tokens in fp32. `values`
         is the relative rounding of keys and values where it is not in `want`."""
         out, mean, size = want
         pairs = min(self.max_rows, self.n) * (self.heads // self.hk)
-        weight = 2.0 ** -22 if pairs <= 64 else 2.0 ** -11
+        weight = 2.0 ** -22 if pairs <= 64 and self.t == torch.float16 else 2.0 ** -11
         terms = self.dim if terms is None else terms
-        score = size * ((terms + 8) * 2.0 ** -24 + values) + 2.0 ** -22
+        keys = 2.0 ** -22 if self.t == torch.float16 else 0.0
+        score = size * ((terms + 8) * 2.0 ** -24 + values + keys) + 2.0 ** -22
         inner = (weight + values + 2 * score + (max(self.kv) + 8) * 2.0 ** -24) * mean + 2.0 ** -40 * low
         half = torch.finfo(self.t).eps / 2
         return half * (out.abs() + inner) + inner + 2.0 ** -25

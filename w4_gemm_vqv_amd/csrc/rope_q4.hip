@@ -81,7 +81,9 @@ __device__ __forceinline__ void store_codes(const float* x, bool has, int piece,
   }
   if (!has) return;
   const float none = __uint_as_float(0x7FC00000u);
-  const _Float16 scale = (_Float16)(nan ? none : (hi - lo) * (1.0f / 15.0f));
+  float step = (hi - lo) * (1.0f / 15.0f);
+  asm("" : "+v"(step));  // rounded to fp32 first: not one instruction with the next rounding
+  const _Float16 scale = (_Float16)(nan ? none : step);
   const _Float16 bias = (_Float16)(nan ? none : lo) + (_Float16)0.0f;  // of zeros: +0
   const float s = (float)scale, b = (float)bias, inv = 1.0f / s;
   unsigned w = 0;
