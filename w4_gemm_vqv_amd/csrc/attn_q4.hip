@@ -21,11 +21,6 @@
 // rounding, 2^-12 of a value. bf16 queries become fp16 times a power of two per
 // row, exact but for values 2^24 below the row's largest.
 
-#ifndef Q4_WAVES
-#define Q4_WAVES (RT == 1 && D <= 128 ? 3 : RT <= 2 && D <= 128 ? 2 : 1)
-#define Q4_STAGES 2
-#define Q4_MIN 8
-#endif
 #include "attn_common.h"
 #include "serve_internal.h"
 
@@ -272,7 +267,7 @@ __device__ __forceinline__ s16x8 scaled_to_half(s16x8 v, int e) {
 }
 
 template <typename T, int D, int RT, int KW, int STAGES, bool FINE>
-__global__ __launch_bounds__(KW * 64, Q4_WAVES) void paged_attn_q4(const AttnArgs a) {
+__global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_attn_q4(const AttnArgs a) {
   typedef _Float16 H;
   constexpr bool HALF = Bits<T>::exponent == Bits<H>::exponent;  // fp16 queries and outputs
   constexpr int BT = KW * 32, DT = D / 16, KS = Keys<D>::STEPS, VG = Values<D>::GROUPS;
@@ -674,36 +669,35 @@ __global__ __launch_bounds__(KW * 64, Q4_WAVES) void paged_attn_q4(const AttnArg
   }
 }
 
-constexpr int kWaves = 4;
-constexpr int stages(int dim) { return dim <= 128 ? Q4_STAGES : 2; }
+// Waves of a work-group, each with blocks of its own.
+constexpr int waves(int dim) { return dim <= 128 ? 4 : 2; }
+constexpr int kStages = 2;
 
 template <typename T, int D, int RT, bool FINE>
 hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
   const int64_t grid = ((int64_t)a.seqs.n_seqs * a.groups * a.splits + 7) / 8 * 8 * a.kv_heads;
-  hipLaunchKernelGGL((paged_attn_q4<T, D, RT, kWaves, stages(D), FINE>), dim3((unsigned)grid),
-                     dim3(kWaves * 64), 0, stream, a);
+  hipLaunchKernelGGL((paged_attn_q4<T, D, RT, waves(D), kStages, FINE>), dim3((unsigned)grid),
+                     dim3(waves(D) * 64), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((paged_attn_join<T, D, kWaves * 32, 16 * RT, false>),
+  hipLaunchKernelGGL((paged_attn_join<T, D, waves(D) * 32, 16 * RT, false>),
                      dim3((unsigned)(a.seqs.n_rows * a.kv_heads * a.group)), dim3(256), 0, stream,
                      a);
   return hipGetLastError();
 }
 
-// Tiles of 16 (row, head) pairs of a work-group, at most.
-constexpr int row_tiles(int dim) { return dim <= 128 ? 4 : 2; }
+// Tiles of 16 (row, head) pairs of a work-group, at most. With four the
+// registers of a wave hold no second block's work and spill (a prompt chunk of
+// 2048 rows over 10240 tokens: 1425 us, with two 730).
+constexpr int kMostTiles = 2;
 
 // Weights in two values: for fp16 outputs of up to 64 pairs. A bf16 output's own
 // rounding is eight times that of a weight in one.
 template <typename T, int D>
 hipError_t launch_dim(const AttnArgs& a, const AttnPlan& p, bool few, hipStream_t stream) {
   constexpr bool HALF = Bits<T>::exponent == Bits<_Float16>::exponent;
-  constexpr int MOST = row_tiles(D);
   if constexpr (HALF) {
-    if (p.mw == MOST && !few) return launch_shape<T, D, MOST, false>(a, stream);
-  }
-  if constexpr (MOST == 4) {
-    if (p.mw == 4) return launch_shape<T, D, 4, HALF>(a, stream);
+    if (!few) return launch_shape<T, D, 2, false>(a, stream);
   }
   return p.mw == 2 ? launch_shape<T, D, 2, HALF>(a, stream)
                    : launch_shape<T, D, 1, HALF>(a, stream);
@@ -731,8 +725,8 @@ int64_t pairs_of(const vqv_seqs& s, int heads, int kv_heads) {
 AttnPlan attn_q4_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int window, int sinks) {
   const int64_t m = pairs_of(s, heads, c.kv_heads);
   AttnPlan p;
-  p.mw = m <= 16 ? 1 : m <= 32 ? 2 : row_tiles(c.dim);
-  p.kw = kWaves;
+  p.mw = m <= 16 ? 1 : kMostTiles;
+  p.kw = waves(c.dim);
   p.kt = 32;
   p.groups = ceil_div(m < 1 ? 1 : m, 16 * p.mw);
   const int bt = p.kw * p.kt;
@@ -746,12 +740,17 @@ AttnPlan attn_q4_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int w
   }
   const int blocks = ceil_div(tokens < 1 ? 1 : tokens, bt);
   const int64_t base = (int64_t)c.kv_heads * s.n_seqs * p.groups;
+  // Blocks of a split: all, where the rows alone fill the GPU; else as many as
+  // leave a work-group to each CU, and no more than 1024 tokens' worth unless
+  // that were more than 16 rounds of work-groups (48 ragged sequences: 164 us,
+  // with 2048 tokens 174, with 4096 201).
+  const int most = 1024 / bt;
   int64_t per = ceil_div(blocks * base, 256);
   if (base >= 512) {
     per = blocks;
-  } else if (per > Q4_MIN) {
+  } else if (per > most) {
     per = ceil_div(blocks * base, window > 0 ? 512 : 4096);
-    if (per < Q4_MIN) per = Q4_MIN;
+    if (per < most) per = most;
   }
   p.split_blocks = per < blocks ? (int)per : blocks;
   p.splits = ceil_div(blocks, p.split_blocks);
