@@ -179,7 +179,7 @@ vqv_status check_sample(int B, int T, int N) {
   if ((double)B * T * N >= 2147483648.0) return VQV_ERR_ARG;
   // The last chunk's tokens are counted in 32 bits, a grid's threads too.
   if (B > 65535 || N > INT32_MAX - (vqv::kVerifyChunk - 1) ||
-      (int64_t)B * T * vqv::verify_chunks(N) >= (1ll << 23) || B * 64ll >= (1ll << 23))
+      (int64_t)B * T * vqv::verify_chunks(N) >= (1ll << 23))
     return VQV_ERR_UNSUPPORTED;
   return VQV_OK;
 }
