@@ -42,12 +42,9 @@ __device__ __forceinline__ f32x4 mfma16<_Float16>(s16x8 a, s16x8 b, f32x4 c) {
                                                 __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
 }
 
-// The adapter of this wave's lane's row, -1 for none, and the slot-th distinct
-// one of the block with the rows that have it (adapter -1: there is none).
-struct Slot {
-  int adapter;
-  uint64_t rows;
-};
+// The adapter of a lane's row, -1 for none, and the slot-th distinct one of the
+// block with the rows that have it (adapter -1: there is none).
+typedef LoraSlot Slot;
 
 __device__ __forceinline__ int adapter_of(const LoraArgs& a, int row) {
   const int e = row < a.M ? a.which[row] : -1;
@@ -59,10 +56,10 @@ __device__ __forceinline__ Slot find_slot(int mine, int slot) {
   for (int s = 0; left != 0; ++s) {
     const int e = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
     const uint64_t rows = __ballot(mine == e);
-    if (s == slot) return Slot{e, rows};
+    if (s == slot) return Slot{rows, e};
     left &= ~rows;
   }
-  return Slot{-1, 0};
+  return Slot{0, -1};
 }
 
 // Place of the k-th set bit of rows (k < their count).
@@ -83,7 +80,50 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int e) {
   return a.ad.ranks ? min(max(a.ad.ranks[e], 0), a.ad.rank) : a.ad.rank;
 }
 
-// RT tiles of 16 ranks. X is the type of x (the adapters', or float).
+// One step of 32 of K, as operands: weights of RT tiles of 16 ranks, and x.
+template <typename T, typename X, int RT>
+struct Step {
+  s16x8 w[RT];
+  f32x4 x[sizeof(X) / 2];
+
+  // Lanes past K (TAIL: there may be some) have zeros.
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const uint16_t* const* weights, const X* row, int k, int K) {
+    const int at = TAIL && k >= K ? 0 : k;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) w[t] = *reinterpret_cast<const s16x8*>(weights[t] + at);
+#pragma unroll
+    for (int e = 0; e < (int)sizeof(X) / 2; ++e)
+      x[e] = *reinterpret_cast<const f32x4*>(row + at + 4 * e);
+    if (TAIL && k >= K) {
+#pragma unroll
+      for (int t = 0; t < RT; ++t) w[t] = s16x8{};
+#pragma unroll
+      for (int e = 0; e < (int)sizeof(X) / 2; ++e) x[e] = f32x4{};
+    }
+  }
+
+  __device__ __forceinline__ void add(f32x4* acc) const {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      if constexpr (sizeof(X) == 2) {
+        acc[t] = mfma16<T>(w[t], __builtin_bit_cast(s16x8, x[0]), acc[t]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const short a = w[t][e];
+          acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32((float)__builtin_bit_cast(T, a),
+                                                        x[e / 4][e % 4], acc[t], 0, 0, 0);
+        }
+      }
+    }
+  }
+};
+
+// RT tiles of 16 ranks. X is the type of x (the adapters', or float). Ranks and
+// rows that are none are loaded from those that are, and not used: no load
+// waits for a condition, and four steps' loads are in flight (chunks of 2100
+// rows, rank 64: TIME_SHRINK us, one step at a time 33).
 template <typename T, typename X, int RT>
 __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(const LoraArgs a, int slots,
                                                                  int splits, int rank_groups) {
@@ -92,13 +132,14 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(const LoraArgs 
   const int split = id % splits;
   id /= splits;
   const int r0 = id % rank_groups * 16 * RT;
+  const bool first = split == 0 && r0 == 0;
   id /= rank_groups;
   const int slot = id % slots, block = id / slots;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quarter = lane >> 4;
   const Slot s = find_slot(adapter_of(a, block * kBlock + lane), slot);
+  if (first && threadIdx.x == 0) a.slots[(int64_t)block * slots + slot] = s;
   if (s.adapter < 0) return;
-  const int rank = rank_of(a, s.adapter);
   const int count = __popcll(s.rows), tiles = (count + 15) / 16;
   const int K = a.ad.K;
 
@@ -108,45 +149,33 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(const LoraArgs 
   const int parts = splits * per_tile;
   const int m = tile * 16 + col;
   const bool real = m < count;
-  const int row = block * kBlock + (real ? nth_row(s.rows, m) : 0);
+  const int row = block * kBlock + nth_row(s.rows, real ? m : 0);
 
   f32x4 acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = f32x4{};
   if (tile < tiles) {
-    const int steps = (K + 31) / 32;
-    const int u0 = (int)((int64_t)steps * part / parts), u1 = (int)((int64_t)steps * (part + 1) / parts);
+    const int steps = (K + 31) / 32, whole = K / 32;
+    const int u0 = (int)((int64_t)steps * part / parts);
+    const int u1 = (int)((int64_t)steps * (part + 1) / parts);
     const X* x = static_cast<const X*>(a.x) + (int64_t)row * K;
-    const uint16_t* w = static_cast<const uint16_t*>(a.ad.a) +
-                        ((int64_t)s.adapter * a.ad.rank + r0 + col) * K;
-    for (int u = u0; u < u1; ++u) {
-      const int k = 32 * u + 8 * quarter;
-      const bool in = k < K;
-      s16x8 wf[RT];
+    const uint16_t* w[RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        wf[t] = s16x8{};
-        if (in && r0 + 16 * t + col < rank)
-          wf[t] = *reinterpret_cast<const s16x8*>(w + (int64_t)16 * t * K + k);
-      }
-      if constexpr (sizeof(X) == 2) {
-        s16x8 xf = {};
-        if (in && real) xf = *reinterpret_cast<const s16x8*>(x + k);
+    for (int t = 0; t < RT; ++t)
+      w[t] = static_cast<const uint16_t*>(a.ad.a) +
+             ((int64_t)s.adapter * a.ad.rank + min(r0 + 16 * t + col, a.ad.rank - 1)) * K;
+    int u = u0;
+    for (; u + 4 <= min(u1, whole); u += 4) {
+      Step<T, X, RT> step[4];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t] = mfma16<T>(wf[t], xf, acc[t]);
-      } else {
-        f32x4 xf[2] = {};
-        if (in && real) {
-          xf[0] = *reinterpret_cast<const f32x4*>(x + k);
-          xf[1] = *reinterpret_cast<const f32x4*>(x + k + 4);
-        }
+      for (int e = 0; e < 4; ++e) step[e].template load<false>(w, x, 32 * (u + e) + 8 * quarter, K);
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            acc[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                (float)__builtin_bit_cast(T, (short)wf[t][e]), xf[e / 4][e % 4], acc[t], 0, 0, 0);
-      }
+      for (int e = 0; e < 4; ++e) step[e].add(acc);
+    }
+    for (; u < u1; ++u) {
+      Step<T, X, RT> step;
+      step.template load<true>(w, x, 32 * u + 8 * quarter, K);
+      step.add(acc);
     }
   }
 #pragma unroll
@@ -177,11 +206,13 @@ struct F4 {  // rows of any 4-byte alignment
   float v[4];
 };
 
-// RB blocks of 32 ranks.
+// RB blocks of 32 ranks. CT tiles of 16 columns are taken at a time, their
+// loads before their products.
 template <typename T, int RB>
 __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs a, int slots,
                                                                  int splits, int col_groups,
                                                                  int cols) {
+  constexpr int CT = RB <= 2 ? 4 : RB == 4 ? 2 : 1;
   int id = blockIdx.x;
   const int c0 = id % col_groups * cols;
   id /= col_groups;
@@ -189,11 +220,11 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quarter = lane >> 4;
   const int N = a.ad.N, end = min(c0 + cols, N);
-  const int mine = adapter_of(a, block * kBlock + lane);
 
   if (slot == 0 && a.out != a.y) {
     // Rows without an adapter stay as they are.
-    uint64_t none = __ballot(mine < 0 && block * kBlock + lane < a.M);
+    const int row = block * kBlock + lane;
+    uint64_t none = __ballot(row < a.M && adapter_of(a, row) < 0);
     while (none != 0) {
       const int64_t row = block * kBlock + __builtin_ctzll(none);
       for (int c = c0 + threadIdx.x; c < end; c += kExpandWaves * 64)
@@ -201,19 +232,18 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
       none &= none - 1;
     }
   }
-  const Slot s = find_slot(mine, slot);
+  const Slot s = a.slots[(int64_t)block * slots + slot];
   if (s.adapter < 0) return;
   const int rank = rank_of(a, s.adapter);
   const float scale = a.ad.scale[s.adapter];
   const int count = __popcll(s.rows), tiles = (count + 15) / 16;
-  // One tile of rows: the waves take turns with its columns. More: a wave takes
-  // a tile (and there are at most four).
+  // One tile of rows: the waves share its columns. More: a wave takes a tile
+  // (and there are at most four).
   const int tile = tiles == 1 ? 0 : wave;
   if (tile >= tiles) return;
-  const int step = tiles == 1 ? 16 * kExpandWaves : 16;
   const int m = tile * 16 + col;
   const bool real = m < count;
-  const int64_t row = block * kBlock + (real ? nth_row(s.rows, m) : 0);
+  const int64_t row = block * kBlock + nth_row(s.rows, real ? m : 0);
 
   // The row's values between the products, as B operands.
   s16x8 low[RB][3];
@@ -228,15 +258,22 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
       for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
       if (real && r < rank) {
         const float* p = a.low + row * a.ad.rank + r;
-        for (int x = 0; x < splits; ++x) {
-          const f32x4 lo = *reinterpret_cast<const f32x4*>(p);
-          const f32x4 hi = *reinterpret_cast<const f32x4*>(p + 4);
+        const int64_t part = (int64_t)a.M * a.ad.rank;
+        for (int x = 0; x < splits; x += 4) {
+          f32x4 lo[4], hi[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[i][e] += lo[e];
-            v[i][4 + e] += hi[e];
+          for (int y = 0; y < 4; ++y) {
+            const float* at = p + min(x + y, splits - 1) * part;
+            lo[y] = *reinterpret_cast<const f32x4*>(at);
+            hi[y] = *reinterpret_cast<const f32x4*>(at + 4);
           }
-          p += (int64_t)a.M * a.ad.rank;
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[i][e] += x + y < splits ? lo[y][e] : 0.0f;
+              v[i][4 + e] += x + y < splits ? hi[y][e] : 0.0f;
+            }
         }
       }
 #pragma unroll
@@ -270,45 +307,67 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
   const uint16_t* w = static_cast<const uint16_t*>(a.ad.b) + (int64_t)s.adapter * N * a.ad.rank;
   const float* y = a.y + row * a.y_stride;
   float* out = a.out + row * a.out_stride;
-  for (int n0 = c0 + (tiles == 1 ? 16 * wave : 0); n0 < end; n0 += step) {
-    const int n = n0 + 4 * quarter;  // of this lane's sums
-    F4 before = {};
-    if (real) {
-      if (n + 4 <= N) {
-        __builtin_memcpy(&before, y + n, 16);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < N) before.v[e] = y[n + e];
-      }
-    }
+  const auto tile_of = [&](int n0, const s16x8* wf, F4 before) {
     f32x4 acc = {};
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int x = 0; x < 3; ++x) acc = mfma16<T>(wf[i], low[i][x], acc);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) before.v[e] = fmaf(acc[e], back, before.v[e]);
+    return before;
+  };
+  // Weights of column n0 + col; those past the rank are zeros.
+  const auto weights = [&](int n, s16x8* wf) {
 #pragma unroll
     for (int i = 0; i < RB; ++i) {
       const int r = 32 * i + 8 * quarter;
-      s16x8 wf = {};
-      if (n0 + col < N && r < rank) {
-        wf = *reinterpret_cast<const s16x8*>(w + (int64_t)(n0 + col) * a.ad.rank + r);
-        if (r + 8 > rank) {
+      wf[i] = *reinterpret_cast<const s16x8*>(w + (int64_t)n * a.ad.rank + (r < a.ad.rank ? r : 0));
+    }
+  };
+  const auto cut = [&](s16x8* wf) {
+    if (rank % 32 == 0 && rank == 32 * RB) return;
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (r + e >= rank) wf[e] = 0;
-        }
-      }
+    for (int i = 0; i < RB; ++i)
 #pragma unroll
-      for (int x = 0; x < 3; ++x) acc = mfma16<T>(wf, low[i][x], acc);
+      for (int e = 0; e < 8; ++e)
+        if (32 * i + 8 * quarter + e >= rank) wf[i][e] = 0;
+  };
+  const int step = tiles == 1 ? 16 * CT * kExpandWaves : 16 * CT;
+  int n0 = c0 + (tiles == 1 ? 16 * CT * wave : 0);
+  for (; n0 + 16 * CT <= end; n0 += step) {
+    s16x8 wf[CT][RB];
+    F4 v[CT];
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+      weights(n0 + 16 * t + col, wf[t]);
+      __builtin_memcpy(&v[t], y + n0 + 16 * t + 4 * quarter, 16);
+    }
+#pragma unroll
+    for (int t = 0; t < CT; ++t) {
+      cut(wf[t]);
+      v[t] = tile_of(n0 + 16 * t, wf[t], v[t]);
     }
     if (real) {
-      F4 r;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r.v[e] = fmaf(acc[e], back, before.v[e]);
-      if (n + 4 <= N) {
-        __builtin_memcpy(out + n, &r, 16);
-      } else {
+      for (int t = 0; t < CT; ++t) __builtin_memcpy(out + n0 + 16 * t + 4 * quarter, &v[t], 16);
+    }
+  }
+  // What is left of the columns, a tile at a time.
+  for (const int stop = min(n0 + 16 * CT, end); n0 < stop; n0 += 16) {
+    s16x8 wf[RB];
+    F4 v = {};
+    const int n = n0 + 4 * quarter;
+    weights(min(n0 + col, N - 1), wf);
+    cut(wf);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < N) out[n + e] = r.v[e];
-      }
+    for (int e = 0; e < 4; ++e)
+      if (n + e < end) v.v[e] = y[n + e];
+    v = tile_of(n0, wf, v);
+    if (real) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < end) out[n + e] = v.v[e];
     }
   }
 }
@@ -335,11 +394,16 @@ Plan plan_of(const vqv_adapters& ad, int M) {
   if (splits > steps / 16) splits = steps / 16;
   if (splits > 8) splits = 8;
   p.splits = splits < 1 ? 1 : splits;
+  // Columns of a work-group of the second kernel: while that leaves two
+  // work-groups to a CU, if an eighth of the slots are taken.
+  const int64_t some = (int64_t)p.blocks * (p.slots / 8 > 1 ? p.slots / 8 : 1);
   p.cols = 256;
-  while (p.cols > 64 && (int64_t)p.blocks * ceil_div(ad.N, p.cols) < 512) p.cols /= 2;
+  while (p.cols > 64 && some * ceil_div(ad.N, p.cols) < 512) p.cols /= 2;
   p.col_groups = ceil_div(ad.N, p.cols);
   return p;
 }
+
+size_t slots_bytes(const Plan& p) { return (size_t)p.blocks * p.slots * sizeof(Slot); }
 
 template <typename T, typename X, int RT>
 hipError_t shrink(const LoraArgs& a, const Plan& p, hipStream_t stream) {
@@ -365,8 +429,10 @@ hipError_t expand(const LoraArgs& a, const Plan& p, hipStream_t stream) {
 }
 
 template <typename T>
-hipError_t launch_type(const LoraArgs& a, bool wide, hipStream_t stream) {
+hipError_t launch_type(LoraArgs a, bool wide, hipStream_t stream) {
   const Plan p = plan_of(a.ad, a.M);
+  a.slots = static_cast<Slot*>(a.workspace);
+  a.low = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + slots_bytes(p));
   const hipError_t e =
       wide ? shrink_tiles<T, float>(a, p, stream) : shrink_tiles<T, T>(a, p, stream);
   if (e != hipSuccess) return e;
@@ -387,7 +453,9 @@ bool lora_grids_fit(const vqv_adapters& ad, int M) {
 }
 
 size_t lora_workspace_bytes(const vqv_adapters& ad, int M) {
-  return M < 1 ? 0 : (size_t)plan_of(ad, M).splits * M * ad.rank * sizeof(float);
+  if (M < 1) return 0;
+  const Plan p = plan_of(ad, M);
+  return slots_bytes(p) + (size_t)p.splits * M * ad.rank * sizeof(float);
 }
 
 hipError_t launch_lora_add(const LoraArgs& a, int act_dtype, hipStream_t stream) {

@@ -291,7 +291,7 @@ vqv_status vqv_lora_add(const void* x, vqv_dtype act_dtype, const vqv_adapters* 
   if (out == y ? out_stride != y_stride : overlaps(out, ob, y, yb)) return VQV_ERR_ARG;
   (void)hipGetLastError();
   return status_of(vqv::launch_lora_add(
-      vqv::LoraArgs{x, a, which, M, y, y_stride, out, out_stride, static_cast<float*>(workspace)},
+      vqv::LoraArgs{x, a, which, M, y, y_stride, out, out_stride, workspace, nullptr, nullptr},
       (int)act_dtype, static_cast<hipStream_t>(hip_stream)));
 }
 

@@ -43,6 +43,11 @@ struct SampleArgs {
 size_t sample_workspace_bytes(int B, int T, int N);
 hipError_t launch_verify_sampled(const SampleArgs& a, hipStream_t stream);
 
+// Rows of a block of 64 that share an adapter (-1: none do).
+struct __attribute__((aligned(16))) LoraSlot {
+  uint64_t rows;
+  int adapter;
+};
 struct LoraArgs {
   const void* x;
   vqv_adapters ad;
@@ -52,7 +57,10 @@ struct LoraArgs {
   int64_t y_stride;
   float* out;
   int64_t out_stride;
-  float* low;  // workspace
+  void* workspace;
+  // In the workspace: the blocks' slots, and the values between the products.
+  LoraSlot* slots;
+  float* low;
 };
 // Whether a call's grids are within 32 bits.
 bool lora_grids_fit(const vqv_adapters& ad, int M);
