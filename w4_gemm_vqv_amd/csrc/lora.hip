@@ -80,6 +80,34 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int e) {
   return a.ad.ranks ? min(max(a.ad.ranks[e], 0), a.ad.rank) : a.ad.rank;
 }
 
+// 16 bytes per lane from global memory to LDS at `lds` (uniform) + 16 * lane;
+// the wait for them is loaded().
+__device__ __forceinline__ void load16_to_lds(const void* from, unsigned lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds), "v"(from)
+               : "memory");
+}
+__device__ __forceinline__ void loaded() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+template <typename V>
+__device__ __forceinline__ V lds_read(unsigned at) {
+  return *(__attribute__((address_space(3))) V*)(uintptr_t)at;
+}
+
+__device__ __forceinline__ unsigned lds_offset(const void* p) {
+  return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// Which 16-byte piece of a staged row of `pieces` holds piece c, so that the
+// same piece of 8 rows lies in different banks (an exchange is its own inverse).
+__device__ __forceinline__ int piece_of(int pieces, int row, int c) {
+  return pieces % 8 == 0   ? c ^ (row & 7)
+         : pieces % 4 == 0 ? c ^ (row >> 1 & 3)
+         : pieces % 2 == 0 ? c ^ (row >> 2 & 1)
+                           : c;
+}
+
 // One step of 32 of K, as operands: weights of RT tiles of 16 ranks, and x.
 template <typename T, typename X, int RT>
 struct Step {
@@ -103,9 +131,11 @@ struct Step {
     }
   }
 
-  __device__ __forceinline__ void add(f32x4* acc) const {
+  // Tiles t0 .. t1 - 1 of ranks.
+  __device__ __forceinline__ void add(f32x4* acc, int t0, int t1) const {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
+      if (t < t0 || t >= t1) continue;
       if constexpr (sizeof(X) == 2) {
         acc[t] = mfma16<T>(w[t], __builtin_bit_cast(s16x8, x[0]), acc[t]);
       } else {
@@ -122,12 +152,20 @@ struct Step {
 
 // RT tiles of 16 ranks. X is the type of x (the adapters', or float). Ranks and
 // rows that are none are loaded from those that are, and not used: no load
-// waits for a condition, and four steps' loads are in flight (chunks of 2100
-// rows, rank 64: TIME_SHRINK us, one step at a time 33).
+// waits for a condition. Few rows: the waves split K, four steps' loads in
+// flight. Several tiles of rows: 128 of K at a time are staged in LDS for all of
+// them, rows of 16 or 32 lanes, as the operands' own loads (16 rows at a time)
+// take the address unit 64 cycles each.
 template <typename T, typename X, int RT>
 __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(const LoraArgs a, int slots,
                                                                  int splits, int rank_groups) {
-  __shared__ f32x4 sums[kShrinkWaves][RT][64];
+  constexpr int KC = 128;                                // of K to a stage
+  constexpr int XP = KC * (int)sizeof(X) / 16, WP = KC * 2 / 16;  // pieces of a row
+  constexpr int XL = kBlock * XP / (64 * kShrinkWaves);  // loads of a wave: x, weights
+  constexpr int WL = (16 * RT * WP + 64 * kShrinkWaves - 1) / (64 * kShrinkWaves);
+  constexpr int STAGE = (XL + WL) * kShrinkWaves * 1024;
+  constexpr int SUMS = kShrinkWaves * RT * 1024;
+  __shared__ __align__(1024) char lds[2 * STAGE > SUMS ? 2 * STAGE : SUMS];
   int id = blockIdx.x;
   const int split = id % splits;
   id /= splits;
@@ -154,38 +192,102 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(const LoraArgs 
   f32x4 acc[RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) acc[t] = f32x4{};
-  if (tile < tiles) {
-    const int steps = (K + 31) / 32, whole = K / 32;
+  const int steps = (K + 31) / 32, whole = K / 32;
+  const X* x = static_cast<const X*>(a.x) + (int64_t)row * K;
+  const uint16_t* weights = static_cast<const uint16_t*>(a.ad.a) + (int64_t)s.adapter * a.ad.rank * K;
+  const uint16_t* w[RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) w[t] = weights + (int64_t)min(r0 + 16 * t + col, a.ad.rank - 1) * K;
+  if (tiles > 1) {
+    const int half = wave % per_tile;  // of two: of the tiles of ranks, or of the steps
+    const int u0 = (int)((int64_t)steps * split / splits);
+    const int u1 = (int)((int64_t)steps * (split + 1) / splits);
+    const int stages = max(min(u1, whole) - u0, 0) / (KC / 32);
+    const char* from[XL + WL];
+#pragma unroll
+    for (int e = 0; e < XL; ++e) {
+      const int p = (e * kShrinkWaves + wave) * 64 + lane, r = p / XP, c = p % XP;
+      const int at = block * kBlock + nth_row(s.rows, min(r, count - 1));
+      from[e] = reinterpret_cast<const char*>(static_cast<const X*>(a.x) + (int64_t)at * K + 32 * u0) +
+                piece_of(XP, r, c) * 16;
+    }
+#pragma unroll
+    for (int e = 0; e < WL; ++e) {
+      const int p = (e * kShrinkWaves + wave) * 64 + lane, r = p / WP, c = p % WP;
+      from[XL + e] = reinterpret_cast<const char*>(
+                         weights + (int64_t)min(r0 + r, a.ad.rank - 1) * K + 32 * u0) +
+                     piece_of(WP, r, c) * 16;
+    }
+    const unsigned base = lds_offset(lds);
+    const auto stage = [&](int i) {
+      const unsigned to = base + (i & 1) * STAGE + wave * 1024;
+#pragma unroll
+      for (int e = 0; e < XL + WL; ++e)
+        load16_to_lds(from[e] + (int64_t)i * KC * (e < XL ? (int)sizeof(X) : 2),
+                      __builtin_amdgcn_readfirstlane(to + e * kShrinkWaves * 1024));
+    };
+    if (stages > 0) stage(0);
+    for (int i = 0; i < stages; ++i) {
+      // Stage i is there for all, and all are done with stage i - 1.
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      if (i + 1 < stages) stage(i + 1);
+      const unsigned xs = base + (i & 1) * STAGE, ws = xs + XL * kShrinkWaves * 1024;
+      const int xr = tile * 16 + col;
+#pragma unroll
+      for (int u = 0; u < KC / 32; ++u) {
+        if (RT == 1 && u / (KC / 64) != half) continue;
+        Step<T, X, RT> step;
+#pragma unroll
+        for (int e = 0; e < (int)sizeof(X) / 2; ++e)
+          step.x[e] = lds_read<f32x4>(
+              xs + (xr * XP + piece_of(XP, xr, (4 * u + quarter) * (int)sizeof(X) / 2 + e)) * 16);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const int wr = 16 * t + col;
+          step.w[t] = lds_read<s16x8>(ws + (wr * WP + piece_of(WP, wr, 4 * u + quarter)) * 16);
+        }
+        if (RT == 1)
+          step.add(acc, 0, 1);
+        else
+          step.add(acc, half * (RT / 2), (half + 1) * (RT / 2));
+      }
+    }
+    if (tile < tiles) {
+      for (int u = u0 + stages * (KC / 32) + half; u < u1; u += 2) {
+        Step<T, X, RT> step;
+        step.template load<true>(w, x, 32 * u + 8 * quarter, K);
+        step.add(acc, 0, RT);
+      }
+    }
+    __syncthreads();
+  } else if (tile < tiles) {
     const int u0 = (int)((int64_t)steps * part / parts);
     const int u1 = (int)((int64_t)steps * (part + 1) / parts);
-    const X* x = static_cast<const X*>(a.x) + (int64_t)row * K;
-    const uint16_t* w[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-      w[t] = static_cast<const uint16_t*>(a.ad.a) +
-             ((int64_t)s.adapter * a.ad.rank + min(r0 + 16 * t + col, a.ad.rank - 1)) * K;
     int u = u0;
     for (; u + 4 <= min(u1, whole); u += 4) {
       Step<T, X, RT> step[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) step[e].template load<false>(w, x, 32 * (u + e) + 8 * quarter, K);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) step[e].add(acc);
+      for (int e = 0; e < 4; ++e) step[e].add(acc, 0, RT);
     }
     for (; u < u1; ++u) {
       Step<T, X, RT> step;
       step.template load<true>(w, x, 32 * u + 8 * quarter, K);
-      step.add(acc);
+      step.add(acc, 0, RT);
     }
   }
+  f32x4* sums = reinterpret_cast<f32x4*>(lds) + lane;  // [wave][t][64]
 #pragma unroll
-  for (int t = 0; t < RT; ++t) sums[wave][t][lane] = acc[t];
+  for (int t = 0; t < RT; ++t) sums[(wave * RT + t) * 64] = acc[t];
   __syncthreads();
   if (tile >= tiles || wave % per_tile != 0 || !real) return;
   float* low = a.low + ((int64_t)split * a.M + row) * a.ad.rank + r0 + 4 * quarter;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    for (int w = 1; w < per_tile; ++w) acc[t] += sums[wave + w][t][lane];
+    for (int w = 1; w < per_tile; ++w) acc[t] += sums[((wave + w) * RT + t) * 64];
     if (r0 + 16 * t + 4 * quarter < a.ad.rank) *reinterpret_cast<f32x4*>(low + 16 * t) = acc[t];
   }
 }
@@ -207,19 +309,27 @@ struct F4 {  // rows of any 4-byte alignment
 };
 
 // RB blocks of 32 ranks. CT tiles of 16 columns are taken at a time, their
-// loads before their products.
-template <typename T, int RB>
+// loads before their products. The lanes of a matrix operand would read 16 rows
+// at a time, 64 bytes of each, which the address unit takes one lane after the
+// other: weights (whole rows, one after the other in memory) come through LDS,
+// and so do the sums, so that y and out are moved in runs of 64 columns.
+template <typename T, int RB, int CT>
 __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs a, int slots,
                                                                  int splits, int col_groups,
                                                                  int cols) {
-  constexpr int CT = RB <= 2 ? 4 : RB == 4 ? 2 : 1;
-  int id = blockIdx.x;
-  const int c0 = id % col_groups * cols;
-  id /= col_groups;
+  constexpr int COLS = 16 * CT;
+  constexpr int SUMS = 16 * (COLS + 4);  // rows 4 apart begin in other banks
+  __shared__ __align__(16) char staged[kExpandWaves][COLS * RB * 64 + SUMS * 4];
+  // Work-groups go to the 8 XCDs in turn: each has columns of its own, whose weights its L2 holds.
+  const int eighth = (col_groups + 7) / 8;
+  int id = blockIdx.x / 8;
+  const int c0 = (id % eighth * 8 + blockIdx.x % 8) * cols;
+  id /= eighth;
   const int slot = id % slots, block = id / slots;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quarter = lane >> 4;
   const int N = a.ad.N, end = min(c0 + cols, N);
+  if (c0 >= N) return;
 
   if (slot == 0 && a.out != a.y) {
     // Rows without an adapter stay as they are.
@@ -305,69 +415,106 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
   }
 
   const uint16_t* w = static_cast<const uint16_t*>(a.ad.b) + (int64_t)s.adapter * N * a.ad.rank;
-  const float* y = a.y + row * a.y_stride;
-  float* out = a.out + row * a.out_stride;
-  const auto tile_of = [&](int n0, const s16x8* wf, F4 before) {
+  const auto product = [&](s16x8* wf) {
+    // Weights past the rank are not used, whatever they are.
+    if (rank != 32 * RB) {
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (32 * i + 8 * quarter + e >= rank) wf[i][e] = 0;
+    }
     f32x4 acc = {};
 #pragma unroll
     for (int i = 0; i < RB; ++i)
 #pragma unroll
       for (int x = 0; x < 3; ++x) acc = mfma16<T>(wf[i], low[i][x], acc);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) before.v[e] = fmaf(acc[e], back, before.v[e]);
-    return before;
+    return acc;
   };
-  // Weights of column n0 + col; those past the rank are zeros.
-  const auto weights = [&](int n, s16x8* wf) {
+
+  const unsigned wl = lds_offset(staged[wave]);
+  float* sums = reinterpret_cast<float*>(staged[wave] + COLS * RB * 64);
+  const int pieces = a.ad.rank / 8;
+  // Pieces of the staged weights: place p has piece `from` of them, in bytes.
+  // p / pieces = p * mul >> 16 for p below 2048.
+  constexpr int LOADS = CT * RB;
+  const int mul = (65535 + pieces) / pieces;
+  int from[LOADS];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      const int r = 32 * i + 8 * quarter;
-      wf[i] = *reinterpret_cast<const s16x8*>(w + (int64_t)n * a.ad.rank + (r < a.ad.rank ? r : 0));
-    }
-  };
-  const auto cut = [&](s16x8* wf) {
-    if (rank % 32 == 0 && rank == 32 * RB) return;
+  for (int e = 0; e < LOADS; ++e) {
+    const int p = min(e * 64 + lane, COLS * pieces - 1), r = p * mul >> 16, c = p - r * pieces;
+    from[e] = (r * pieces + piece_of(pieces, r, c)) * 16;
+  }
+  // This lane's rows of y and out, and its 4 columns of them: a row to 4 CT lanes.
+  const int of_row = lane / (4 * CT), of_col = lane % (4 * CT) * 4;
+  int64_t rows[CT];
+  float by[CT];
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+  for (int i = 0; i < CT; ++i) {
+    const int r = 16 / CT * i + of_row;
+    rows[i] = (int64_t)block * kBlock + __shfl((int)(row - (int64_t)block * kBlock), r);
+    by[i] = __shfl(back, r);
+  }
+  const int step = tiles == 1 ? COLS * kExpandWaves : COLS;
+  int n0 = c0 + (tiles == 1 ? COLS * wave : 0);
+  for (; n0 + COLS <= end; n0 += step) {
+    // COLS rows of weights, as they lie.
+    const char* rows_at = reinterpret_cast<const char*>(w + (int64_t)n0 * a.ad.rank);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last reads are done
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (32 * i + 8 * quarter + e >= rank) wf[i][e] = 0;
-  };
-  const int step = tiles == 1 ? 16 * CT * kExpandWaves : 16 * CT;
-  int n0 = c0 + (tiles == 1 ? 16 * CT * wave : 0);
-  for (; n0 + 16 * CT <= end; n0 += step) {
-    s16x8 wf[CT][RB];
+    for (int e = 0; e < LOADS; ++e)
+      if (e * 64 < COLS * pieces)
+        load16_to_lds(rows_at + from[e], __builtin_amdgcn_readfirstlane(wl + e * 1024));
     F4 v[CT];
 #pragma unroll
-    for (int t = 0; t < CT; ++t) {
-      weights(n0 + 16 * t + col, wf[t]);
-      __builtin_memcpy(&v[t], y + n0 + 16 * t + 4 * quarter, 16);
-    }
+    for (int i = 0; i < CT; ++i)
+      __builtin_memcpy(&v[i], a.y + rows[i] * a.y_stride + n0 + of_col, 16);
+    loaded();
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
-      cut(wf[t]);
-      v[t] = tile_of(n0 + 16 * t, wf[t], v[t]);
-    }
-    if (real) {
+      s16x8 wf[RB];
+      const int r = 16 * t + col;
 #pragma unroll
-      for (int t = 0; t < CT; ++t) __builtin_memcpy(out + n0 + 16 * t + 4 * quarter, &v[t], 16);
+      for (int i = 0; i < RB; ++i) {
+        const int c = 4 * i + quarter;
+        wf[i] = lds_read<s16x8>(wl + (r * pieces + piece_of(pieces, r, c < pieces ? c : 0)) * 16);
+      }
+      const f32x4 acc = product(wf);
+      *reinterpret_cast<f32x4*>(sums + col * (COLS + 4) + 16 * t + 4 * quarter) = acc;
+    }
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      const int m = 16 / CT * i + of_row;
+      const f32x4 acc = *reinterpret_cast<const f32x4*>(sums + m * (COLS + 4) + of_col);
+      f32x4 r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = fmaf(acc[e], by[i], v[i].v[e]);
+      // Written once and not read again here: past the L2, which holds weights.
+      if (tile * 16 + m < count) {
+        typedef __attribute__((ext_vector_type(4), aligned(4))) float f32x4_4;
+        __builtin_nontemporal_store(
+            (f32x4_4)r, reinterpret_cast<f32x4_4*>(a.out + rows[i] * a.out_stride + n0 + of_col));
+      }
     }
   }
   // What is left of the columns, a tile at a time.
-  for (const int stop = min(n0 + 16 * CT, end); n0 < stop; n0 += 16) {
+  const float* y = a.y + row * a.y_stride;
+  float* out = a.out + row * a.out_stride;
+  for (const int stop = min(n0 + COLS, end); n0 < stop; n0 += 16) {
     s16x8 wf[RB];
-    F4 v = {};
     const int n = n0 + 4 * quarter;
-    weights(min(n0 + col, N - 1), wf);
-    cut(wf);
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (n + e < end) v.v[e] = y[n + e];
-    v = tile_of(n0, wf, v);
+    for (int i = 0; i < RB; ++i) {
+      const int r = 32 * i + 8 * quarter;
+      wf[i] = *reinterpret_cast<const s16x8*>(w + (int64_t)min(n0 + col, N - 1) * a.ad.rank +
+                                              (r < a.ad.rank ? r : 0));
+    }
+    const f32x4 acc = product(wf);
     if (real) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (n + e < end) out[n + e] = v.v[e];
+        if (n + e < end) out[n + e] = fmaf(acc[e], back, y[n + e]);
     }
   }
 }
@@ -394,11 +541,12 @@ Plan plan_of(const vqv_adapters& ad, int M) {
   if (splits > steps / 16) splits = steps / 16;
   if (splits > 8) splits = 8;
   p.splits = splits < 1 ? 1 : splits;
-  // Columns of a work-group of the second kernel: while that leaves two
-  // work-groups to a CU, if an eighth of the slots are taken.
+  // Columns of a work-group of the second kernel: 64 to a wave, or 16 where that
+  // leaves fewer than one work-group to a CU if an eighth of the slots are taken,
+  // or the weights of 64 would take all of a CU's LDS.
   const int64_t some = (int64_t)p.blocks * (p.slots / 8 > 1 ? p.slots / 8 : 1);
-  p.cols = 256;
-  while (p.cols > 64 && some * ceil_div(ad.N, p.cols) < 512) p.cols /= 2;
+  const bool few = ad.rank > 128 || some * ceil_div(ad.N, 64 * kExpandWaves) < 256;
+  p.cols = kExpandWaves * (few ? 16 : 64);
   p.col_groups = ceil_div(ad.N, p.cols);
   return p;
 }
@@ -420,12 +568,20 @@ hipError_t shrink_tiles(const LoraArgs& a, const Plan& p, hipStream_t stream) {
   return shrink<T, X, 4>(a, p, stream);
 }
 
-template <typename T, int RB>
+template <typename T, int RB, int CT>
 hipError_t expand(const LoraArgs& a, const Plan& p, hipStream_t stream) {
-  const int64_t grid = (int64_t)p.blocks * p.slots * p.col_groups;
-  hipLaunchKernelGGL((lora_expand<T, RB>), dim3((unsigned)grid), dim3(kExpandWaves * 64), 0,
+  const int64_t grid = (int64_t)p.blocks * p.slots * ((p.col_groups + 7) / 8 * 8);
+  hipLaunchKernelGGL((lora_expand<T, RB, CT>), dim3((unsigned)grid), dim3(kExpandWaves * 64), 0,
                      stream, a, p.slots, p.splits, p.col_groups, p.cols);
   return hipGetLastError();
+}
+
+template <typename T, int RB>
+hipError_t expand_cols(const LoraArgs& a, const Plan& p, hipStream_t stream) {
+  if constexpr (RB < 8) {
+    if (p.cols == 64 * kExpandWaves) return expand<T, RB, 4>(a, p, stream);
+  }
+  return expand<T, RB, 1>(a, p, stream);
 }
 
 template <typename T>
@@ -437,10 +593,10 @@ hipError_t launch_type(LoraArgs a, bool wide, hipStream_t stream) {
       wide ? shrink_tiles<T, float>(a, p, stream) : shrink_tiles<T, T>(a, p, stream);
   if (e != hipSuccess) return e;
   const int blocks = ceil_div(a.ad.rank, 32);
-  if (blocks == 1) return expand<T, 1>(a, p, stream);
-  if (blocks == 2) return expand<T, 2>(a, p, stream);
-  if (blocks <= 4) return expand<T, 4>(a, p, stream);
-  return expand<T, 8>(a, p, stream);
+  if (blocks == 1) return expand_cols<T, 1>(a, p, stream);
+  if (blocks == 2) return expand_cols<T, 2>(a, p, stream);
+  if (blocks <= 4) return expand_cols<T, 4>(a, p, stream);
+  return expand_cols<T, 8>(a, p, stream);
 }
 
 }  // namespace
@@ -449,7 +605,7 @@ bool lora_grids_fit(const vqv_adapters& ad, int M) {
   if (M < 1) return true;
   const Plan p = plan_of(ad, M);
   const int64_t groups = (int64_t)p.blocks * p.slots;
-  return groups * p.rank_groups * p.splits < (1ll << 22) && groups * p.col_groups < (1ll << 23);
+  return groups * p.rank_groups * p.splits < (1ll << 22) && groups * (p.col_groups + 7) < (1ll << 23);
 }
 
 size_t lora_workspace_bytes(const vqv_adapters& ad, int M) {
