@@ -94,6 +94,8 @@ vqv_status vqv_cache_q4_read(const vqv_cache_q4* cache, int layer, const vqv_seq
  * largest so far, are rounded once too; for fp16 outputs they are two numbers
  * (to 2^-22) where max_rows rows of a key head's queries are 64 or fewer.
  * Weights 2^29 below the largest are off by up to 2^-39 of it.
+ * The workspace of large bf16 calls without a window (prompt chunks) holds the
+ * tokens of their sequences in fp16, 1 GiB at most; fp16 calls use less of it.
  */
 size_t vqv_paged_attn_q4_workspace_bytes(const vqv_cache_q4* cache, const vqv_seqs* seqs,
                                          int heads, int window, int sinks);
@@ -122,8 +124,8 @@ vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4*
  *                [0, N) is not accepted.
  *   draft_probs  [B, T-1, N] fp32, or NULL: the drafts were not drawn, q_i is 1
  *                at the draft and 0 elsewhere. 16-byte aligned. Rows are used as
- *                they are; a NaN in them counts as 1 at the draft's place (it is
- *                rejected) and takes its token out of r.
+ *                they are; a draft whose own entry is NaN is rejected, and a
+ *                token whose entry is NaN is not drawn from r.
  *   draft_len    [B] int32 or NULL, as in vqv_verify_ex.
  *   temperature  [B] fp32, or NULL: 1. Where it is 0 or less (or NaN) the
  *                request is greedy: p is 1 at the row's argmax as vqv_verify
@@ -181,7 +183,8 @@ typedef struct {
  *              aligned (16-byte aligned rows are faster). out may be y itself
  *              with the same stride, else they may not overlap.
  *   M          >= 0, M * N and M * K < 2^40, M < 2^22 (else
- *              VQV_ERR_UNSUPPORTED).
+ *              VQV_ERR_UNSUPPORTED, as where a grid were too large: it is not
+ *              while (M + 64) * min(n, 64) * (N + 1024) < 2^34).
  *   workspace  vqv_lora_add_workspace_bytes(adapters, M) bytes, 16-byte
  *              aligned; may be NULL when that is 0.
  * Products of 16-bit values are exact; sums, and the values between the two

@@ -522,3 +522,148 @@ def test_refuses_wrong_tensors(vqv):
         vqv.vqv_rope_append_q4(c.qd, kv[:1], kv, c.cache, c.seqs, rope)
     with pytest.raises(ValueError):
         vqv.vqv_cache_q4_read(c.cache, c.seqs, k_out=torch.empty(2, 1, 32, device="cuda"))
+
+
+# ---- many rows of bf16: read through a 16-bit copy in the workspace ----
+
+
+def planned(rows, heads, **kw):
+    """A case whose max_kv, far above the real lengths, makes the call large enough for the copy."""
+    return Case(rows=rows, heads=heads, max_kv=2 ** 27 // (max(rows) * heads) + 1, **kw)
+
+
+def copies(c, vqv):
+    need = vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads)
+    return need >= 2 * max(c.kv) * c.hk * c.dim * 2 + c.n * c.heads * c.dim * 4
+
+
+COPIED = [
+    dict(rows=[200], kv=[300], heads=8, hk=2, dim=128, ps=16),
+    dict(rows=[129], kv=[129], heads=4, hk=1, dim=64, ps=1, layout="head"),
+    dict(rows=[260], kv=[411], heads=6, hk=3, dim=80, ps=20, layout="gap"),
+    dict(rows=[171], kv=[800], heads=12, hk=4, dim=96, ps=24),
+    dict(rows=[512], kv=[600], heads=2, hk=2, dim=192, ps=64, layers=3, layer=1),
+    dict(rows=[150], kv=[1201], heads=8, hk=2, dim=256, ps=1000),
+    # 512 pairs and more, fewer, none, just as many
+    dict(rows=[130, 3, 0, 128, 1, 127], kv=[400, 90, 5, 128, 700, 130], heads=8, hk=2, dim=128, ps=16),
+    dict(rows=[1, 2, 1], kv=[70, 300, 9], heads=600, hk=1, dim=64, ps=8),   # rows of 600 pairs
+    dict(rows=[1, 0, 0, 1, 0], kv=[40, 5, 0, 33, 2], heads=1024, hk=1, dim=96, ps=16),
+    dict(rows=[0, 1, 0, 0], kv=[7, 40, 3, 33], heads=600, hk=1, dim=128, ps=16),
+]
+
+
+@pytest.mark.parametrize("case", COPIED, ids=lambda c: f"{c['rows']}kv{c['kv']}h{c['heads']}/{c['hk']}d{c['dim']}p{c['ps']}")
+def test_copied_attention(vqv, case):
+    c = planned(**case)
+    c.close(c.run(vqv), c.want())
+    assert copies(c, vqv)
+    c.close(c.run(vqv, 100, 7), c.want(100, 7))
+
+
+def test_copied_or_longer_than_planned(vqv):
+    """Of one call: sequences that fit the copy, one that is longer, one of few rows; then pages that
+    are not there."""
+    c = Case(rows=[700, 640, 5, 700], kv=[3000, 12100, 800, 700], heads=16, hk=2, dim=64, ps=16, max_kv=12000)
+    c.close(c.run(vqv), c.want(), low=5.0 * 12100)
+    assert copies(c, vqv)
+    c.table[0][3], c.table[0][4], c.table[1][0], c.table[3][18] = -1, c.pages, 1 << 30, -9
+    c.close(c.run(vqv), c.want(), low=5.0 * 12100)
+    c.table[3] = [-1] * len(c.table[3])
+    got = c.run(vqv)
+    c.close(got, c.want(), low=5.0 * 12100)
+    assert (got[1345:] == 0).all()
+
+
+def test_copied_lengths(vqv):
+    """kv_len below the rows, zero, past the table; rows past max_rows."""
+    c = planned(rows=[300, 290, 280], kv=[640, 300, 290], heads=4, hk=2, dim=64, ps=16)
+    c.kv = [700, 3, 0]
+    got = c.run(vqv)
+    c.close(got, c.want())
+    assert (got[300:587] == 0).all() and (got[590:] == 0).all()
+    c = Case(rows=[400], kv=[450], heads=4, hk=2, dim=64, ps=16, max_rows=270, max_kv=2 ** 17)
+    got, want = c.run(vqv), c.want()
+    assert (got[270:] == 9.0).all()
+    c.n = 270
+    c.close(got[:270], tuple(x[:270] for x in want))
+
+
+def test_copied_nan(vqv):
+    """Hidden tokens may hold anything, a NaN that is seen comes out."""
+    nan = float("nan")
+    for dim in (128, 192):
+        c = planned(rows=[300], kv=[700], heads=4, hk=2, dim=dim, ps=16)
+        clean = c.run(vqv)
+        for t in (699, 550):
+            c.set(0, t, torch.full((1, 2, dim), nan), torch.full((1, 2, dim), nan))
+        got = c.run(vqv)
+        assert torch.equal(got[:150], clean[:150]) and got[150:].isnan().all()
+        c = planned(rows=[300], kv=[700], heads=4, hk=2, dim=dim, ps=16)
+        v = q4.unpack(c.rv[0, c.table[0][0], 5], dim).float()[None]
+        v[0, 0, 40] = nan           # of one group of one head
+        c.set(0, 5, v=v)
+        got = c.run(vqv)
+        assert got[:, :2, 32:64].isnan().all()
+        assert got[:, 2:].isfinite().all() and got[:, :2, :32].isfinite().all() and got[:, :2, 64:].isfinite().all()
+
+
+def test_copied_scores_of_any_size(vqv):
+    for dim in (128, 192):
+        c = planned(rows=[300], kv=[500], heads=4, hk=2, dim=dim, ps=16, seed=5)
+        plain = c.q.clone()
+        for size in (12.0, 1e-30, 1e-38, 1e15):
+            c.q = (plain.float() * size).to(c.t)
+            scale = 1.0 if size == 12.0 or size < 1e-35 else 0.125 / size
+            c.close(c.run(vqv, scale=scale), c.want(scale=scale))
+        c.q = plain
+        c.q[0] = 0
+        c.q[1, 0, 3:] = 0
+        c.q[2, :, 0] = 1e6          # beside it the others of the row are small
+        c.close(c.run(vqv, scale=1e-6), c.want(scale=1e-6))
+        for size in (1e6, 1e30):    # one token takes all
+            c.q = torch.full_like(c.q, size)
+            k = torch.zeros(500, 2, dim)
+            k[:] = torch.arange(500.0)[:, None, None] % 450
+            c.set(0, 0, k)
+            assert torch.equal(c.run(vqv, scale=1.0), c.want(scale=1.0)[0].to(c.t))
+
+
+def test_copied_on_streams_and_in_graphs(vqv):
+    """Two graphs that share one workspace, replayed in turn; nothing is taken from the workspace."""
+    c = planned(rows=[300, 6], kv=[500, 1700], heads=4, hk=2, dim=128, ps=16)
+    want = c.run(vqv)
+    assert copies(c, vqv)
+    assert torch.equal(c.run(vqv, stream=torch.cuda.Stream()), want)
+    need = vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    window = c.run(vqv, 90, 3)
+    outs, graphs = [], []
+    for args in ({}, dict(window=90, sinks=3)):
+        out = torch.empty(c.q.shape, dtype=c.t, device="cuda")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            vqv.vqv_paged_attn_q4(c.qd, c.cache, c.seqs, scale=c.scale, out=out, workspace=ws, **args)
+        outs.append(out)
+        graphs.append(graph)
+    for i in range(4):
+        for out in outs:
+            out.zero_()
+        ws.fill_(255 if i % 2 else 0)
+        torch.cuda.synchronize()
+        graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0].cpu(), want) and torch.equal(outs[1].cpu(), window)
+
+
+def test_copied_workspace(vqv):
+    """A call needs the whole workspace; fp16 takes no copy and less."""
+    c = planned(rows=[300], kv=[500], heads=4, hk=2, dim=128, ps=16)
+    c.run(vqv)
+    need = vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads)
+    out = torch.empty(c.q.shape, dtype=c.t, device="cuda")
+    with pytest.raises(Exception, match="(?i)workspace"):
+        vqv.vqv_paged_attn_q4(c.qd, c.cache, c.seqs, scale=c.scale, out=out,
+                              workspace=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
+    h = planned(rows=[300], kv=[500], heads=4, hk=2, dim=128, ps=16, dtype="fp16")
+    h.close(h.run(vqv), h.want())

@@ -22,7 +22,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 SOURCES = ["vqv_api.hip", "qgemm.hip", "qgemm_m8.hip", "qgemm_m16.hip", "qgemm_v.hip",
            "verify.hip", "round_api.hip", "rope.hip", "attn.hip", "cache.hip", "logits.hip",
-           "serve_api.hip", "rope_q4.hip", "attn_q4.hip", "sample.hip", "lora.hip"]
+           "serve_api.hip", "rope_q4.hip", "attn_q4.hip", "copy_q4.hip",
+           "sample.hip", "lora.hip"]
 LIB = os.path.join(PKG, "libvqv.so")
 ARCH = "gfx950"
 

@@ -48,7 +48,9 @@
 namespace vqv {
 namespace {
 
-template <typename T, int D, int MW, int KW, int KT, int STAGES>
+// T is the type of the cache and of the matrix products, TO that of queries and
+// outputs: the same, or bf16 over an fp16 cache (one that was held in 4 bits).
+template <typename T, int D, int MW, int KW, int KT, int STAGES, typename TO>
 __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void paged_attn(
     const AttnArgs a) {
   constexpr int NW = MW * KW, BT = KW * KT, DC = D / 8, DS = D / 16, DB = (D + 31) / 32;
@@ -87,6 +89,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
   const Tiles tile = tiles_of<PAIRS>(group, tiles);
   const int pos0 = max(a.seqs.kv_len[b], 0) - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
   const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
+  if (not_of_this_call(a, b)) return;
   const Blocks blocks =
       visible_blocks<BT>(pos0 + tile.first * ROWS / g,
                          pos0 + (min((tile.second + 1) * ROWS, pairs) - 1) / g, kv_len, a.window,
@@ -117,6 +120,23 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
       qf[s] = *reinterpret_cast<const s16x8*>(static_cast<const uint16_t*>(a.q) + mine.index * D +
                                               16 * s + 8 * (lane >> 5));
   }
+
+  // bf16 queries of fp16 products: times a power of two for each row, which the
+  // scale of its scores takes back.
+  constexpr bool SAME = Bits<T>::exponent == Bits<TO>::exponent;
+  int shift_q = 0;
+  if constexpr (!SAME) {
+    unsigned top = 0;
+#pragma unroll
+    for (int s = 0; s < DS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, (unsigned)(unsigned short)qf[s][e] & 0x7FFFu);
+    const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+    shift_q = shift_to_half(max(both[0], both[1]));
+#pragma unroll
+    for (int s = 0; s < DS; ++s) qf[s] = scaled_to_half(qf[s], shift_q);
+  }
+  const float scale_log2 = SAME ? a.scale_log2 : ldexpf(a.scale_log2, -shift_q);
 
   f32x16 o[DB];
 #pragma unroll
@@ -266,7 +286,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
     // outputs are off by 9 to 18 % more, and a single large weight by half a step.)
     if (__any(top > mx)) {
       const float now = fmaxf(mx, top);
-      const float back = exp_of(mx, now, a.scale_log2);
+      const float back = exp_of(mx, now, scale_log2);
       mx = now;
       sum *= back;
 #pragma unroll
@@ -275,7 +295,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
         for (int i = 0; i < 16; ++i) o[d][i] *= back;
     }
     const float base = mx == -__builtin_inff() ? 0.0f : mx;
-    float shift = fmaf(base, a.scale_log2, -Bits<T>::top);
+    float shift = fmaf(base, scale_log2, -Bits<T>::top);
     // Of a large maximum the shift's rounding would be the weights' size: the
     // maximum is then taken off the scores first, which is exact near it.
     if (__any(fabsf(shift) > kLarge)) {
@@ -296,7 +316,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           p[e] = __builtin_amdgcn_exp2f(
-              fmaf(s[u / 2][8 * (u & 1) + 2 * i + e], a.scale_log2, -shift));
+              fmaf(s[u / 2][8 * (u & 1) + 2 * i + e], scale_log2, -shift));
         if (FINE) {
           const u32x2 w = split2<T>(p[0], p[1]);
           high[i] = w[0];
@@ -372,7 +392,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
       if (kw < w) {
         const float om = mine[DB * 16 * 64], os = mine[(DB * 16 + 1) * 64];
         const float top = fmaxf(mx, om);
-        const float fa = exp_of(mx, top, a.scale_log2), fb = exp_of(om, top, a.scale_log2);
+        const float fa = exp_of(mx, top, scale_log2), fb = exp_of(om, top, scale_log2);
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -396,8 +416,8 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
       for (int i = 0; i < 4; ++i) {
         const int col = 32 * d + 8 * i + 4 * half;
         if (col < D) {
-          u32x2 w = {pack2<T>(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
-                     pack2<T>(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+          u32x2 w = {pack2<TO>(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
+                     pack2<TO>(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
           *reinterpret_cast<u32x2*>(out + col) = w;
         }
       }
@@ -414,20 +434,20 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
               f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
       }
     if (half == 0) {
-      a.part_ml[2 * at] = mx;
+      a.part_ml[2 * at] = SAME ? mx : ldexpf(mx, -shift_q);
       a.part_ml[2 * at + 1] = sum;
     }
   }
 }
 
-template <typename T, int D, int MW, int KW, int KT, int STAGES>
+template <typename T, int D, int MW, int KW, int KT, int STAGES, typename TO = T>
 hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
   const int64_t grid = (int64_t)a.kv_heads * a.seqs.n_seqs * a.groups * a.splits;
-  hipLaunchKernelGGL((paged_attn<T, D, MW, KW, KT, STAGES>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((paged_attn<T, D, MW, KW, KT, STAGES, TO>), dim3((unsigned)grid),
                      dim3(MW * KW * 64), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((paged_attn_join<T, D, KW * KT, MW == 8 ? 128 : 32 * MW, MW == 8>),
+  hipLaunchKernelGGL((paged_attn_join<TO, D, KW * KT, MW == 8 ? 128 : 32 * MW, MW == 8>),
                      dim3((unsigned)(a.seqs.n_rows * a.kv_heads * a.group)), dim3(256), 0, stream,
                      a);
   return hipGetLastError();
@@ -459,6 +479,28 @@ hipError_t launch_type(const AttnArgs& a, int dim, const AttnPlan& p, hipStream_
     case 128: return launch_dim<T, 128>(a, p, stream);
     case 192: return launch_dim<T, 192>(a, p, stream);
     default: return launch_dim<T, 256>(a, p, stream);
+  }
+}
+
+// bf16 queries over the fp16 copy of a 4-bit cache: plans of many rows alone.
+template <int D>
+hipError_t launch_copied_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+  if constexpr (D <= 128) {
+    if (p.mw == 8) return launch_shape<_Float16, D, 8, 1, 64, 4, __bf16>(a, stream);
+    return launch_shape<_Float16, D, 4, 1, 64, 2, __bf16>(a, stream);
+  } else {
+    return launch_shape<_Float16, D, 4, 1, 32, 4, __bf16>(a, stream);
+  }
+}
+
+hipError_t launch_copied(const AttnArgs& a, int dim, const AttnPlan& p, hipStream_t stream) {
+  switch (dim) {
+    case 64: return launch_copied_dim<64>(a, p, stream);
+    case 80: return launch_copied_dim<80>(a, p, stream);
+    case 96: return launch_copied_dim<96>(a, p, stream);
+    case 128: return launch_copied_dim<128>(a, p, stream);
+    case 192: return launch_copied_dim<192>(a, p, stream);
+    default: return launch_copied_dim<256>(a, p, stream);
   }
 }
 
@@ -515,9 +557,11 @@ size_t attn_partial_bytes(const vqv_cache& c, const vqv_seqs& s, int heads, cons
   return (size_t)s.n_rows * heads * p.splits * (c.dim + 2) * sizeof(float);
 }
 
-hipError_t launch_paged_attn(const void* q, const vqv_cache& c, int layer, const vqv_seqs& seqs,
-                             int heads, float scale, int window, int sinks, void* out,
-                             void* workspace, const AttnPlan& plan, hipStream_t stream) {
+namespace {
+
+AttnArgs args_of(const void* q, const vqv_cache& c, int layer, const vqv_seqs& seqs, int heads,
+                 float scale, int window, int sinks, void* out, void* workspace,
+                 const AttnPlan& plan) {
   AttnArgs a = attn_args(q, out, seqs, c.page_size, c.pages, c.kv_heads, heads, c.dim, scale,
                          window, sinks, workspace, plan);
   a.k = static_cast<const uint16_t*>(c.k) + layer * c.layer_stride;
@@ -525,8 +569,27 @@ hipError_t launch_paged_attn(const void* q, const vqv_cache& c, int layer, const
   a.page_units = (unsigned)(c.page_stride >> 3);
   a.slot_units = (unsigned)(c.slot_stride >> 3);
   a.head_units = (unsigned)(c.head_stride >> 3);
+  return a;
+}
+
+}  // namespace
+
+hipError_t launch_paged_attn(const void* q, const vqv_cache& c, int layer, const vqv_seqs& seqs,
+                             int heads, float scale, int window, int sinks, void* out,
+                             void* workspace, const AttnPlan& plan, hipStream_t stream) {
+  const AttnArgs a =
+      args_of(q, c, layer, seqs, heads, scale, window, sinks, out, workspace, plan);
   return c.dtype == VQV_BF16 ? launch_type<__bf16>(a, c.dim, plan, stream)
                              : launch_type<_Float16>(a, c.dim, plan, stream);
+}
+
+hipError_t launch_paged_attn_copied(const void* q, const vqv_cache& c, const vqv_seqs& seqs,
+                                    int heads, float scale, int copied_len, void* out,
+                                    void* workspace, const AttnPlan& plan, hipStream_t stream) {
+  AttnArgs a = args_of(q, c, 0, seqs, heads, scale, 0, 0, out, workspace, plan);
+  a.which = kCopied;
+  a.copied_len = copied_len;
+  return launch_copied(a, c.dim, plan, stream);
 }
 
 }  // namespace vqv

@@ -23,6 +23,13 @@ typedef __attribute__((ext_vector_type(4))) float f32x4;
 constexpr unsigned kNoPlace = ~0u;
 constexpr float kLarge = 4096.0f;  // a shift below it is off by 2^-13 at most
 
+// The sequences of a launch. Of a 4-bit cache those of many rows are read through
+// a 16-bit copy (kCopied), the others from the cache itself.
+enum { kAll, kCopied, kOthers };
+
+// (row, head) pairs of one key head from which a sequence's tokens are copied.
+constexpr int kCopiedPairs = 512;
+
 struct AttnArgs {
   const void* q;
   void* out;
@@ -36,6 +43,7 @@ struct AttnArgs {
   float scale_log2;
   int window, sinks;
   int groups, split_blocks, splits;  // work-groups over a sequence's rows; of its tokens
+  int which, copied_len;             // of kAll, kCopied, kOthers; tokens that a copy holds
   float* part;  // [n_rows * heads][splits][dim] sums, then [..][splits][2] (max, sum)
   float* part_ml;
 };
@@ -108,6 +116,25 @@ __device__ __forceinline__ u32x2 split2<_Float16>(float a, float b) {
   return u32x2{__builtin_bit_cast(unsigned, r),
                pack2<_Float16>(__builtin_amdgcn_fmed3f(a - (float)r[0], least, a),
                                __builtin_amdgcn_fmed3f(b - (float)r[1], least, b))};
+}
+
+// The power of two that brings a bf16 row, of which `top` is the largest
+// magnitude's bits, to between 2^10 and 2^11.
+__device__ __forceinline__ int shift_to_half(unsigned top) {
+  const int e = max((int)(top >> 7), 1) - 127;
+  return top != 0 && top < 0x7F80u ? 10 - e : 0;
+}
+
+// 8 bf16 values as fp16 times 2^e.
+__device__ __forceinline__ s16x8 scaled_to_half(s16x8 v, int e) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = ldexpf(__uint_as_float((unsigned)(unsigned short)v[2 * i] << 16), e);
+    const float b = ldexpf(__uint_as_float((unsigned)(unsigned short)v[2 * i + 1] << 16), e);
+    r[i] = pack2<_Float16>(a, b);
+  }
+  return __builtin_bit_cast(s16x8, r);
 }
 
 // Not 0 where one of two packed values is an infinity or NaN: an exponent of
@@ -342,6 +369,15 @@ __device__ __forceinline__ int tokens_of(const AttnArgs& a, int kv_len) {
   return (int)min((int64_t)kv_len, min(room, (int64_t)1 << 30));
 }
 
+__device__ __forceinline__ bool is_copied(const vqv_seqs& s, int b, int group, int copied_len) {
+  const int n = min(min(s.row_start[b + 1], s.n_rows) - max(s.row_start[b], 0), s.max_rows);
+  return n * group >= kCopiedPairs && s.kv_len[b] <= copied_len;
+}
+
+__device__ __forceinline__ bool not_of_this_call(const AttnArgs& a, int b) {
+  return a.which != kAll && is_copied(a.seqs, b, a.group, a.copied_len) != (a.which == kCopied);
+}
+
 // Blocks of a split: the plan's, or more where a sequence is longer than the
 // plan was made for.
 __device__ __forceinline__ int blocks_of_split(const AttnArgs& a, int all) {
@@ -381,6 +417,7 @@ __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a) {
   const int g = a.group, tiles = (n * g + ROWS - 1) / ROWS;
   const int pos0 = max(a.seqs.kv_len[b], 0) - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
   const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
+  if (not_of_this_call(a, b)) return;
   const Tiles tile =
       tiles_of<PAIRS>(group_of<PAIRS>(((r - row0) * g + head % g) / ROWS, tiles), tiles);
   const Blocks blocks =
@@ -450,6 +487,8 @@ inline AttnArgs attn_args(const void* q, void* out, const vqv_seqs& seqs, int pa
   a.groups = plan.groups;
   a.split_blocks = plan.split_blocks;
   a.splits = plan.splits;
+  a.which = kAll;
+  a.copied_len = 0;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part + (size_t)seqs.n_rows * heads * plan.splits * dim;
   return a;

@@ -254,18 +254,6 @@ __device__ __forceinline__ float max_of_quarters(float x) {
   return max_of_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
 }
 
-// 8 query values as fp16 times 2^e.
-__device__ __forceinline__ s16x8 scaled_to_half(s16x8 v, int e) {
-  u32x4 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = ldexpf(__uint_as_float((unsigned)(unsigned short)v[2 * i] << 16), e);
-    const float b = ldexpf(__uint_as_float((unsigned)(unsigned short)v[2 * i + 1] << 16), e);
-    r[i] = pack2<_Float16>(a, b);
-  }
-  return __builtin_bit_cast(s16x8, r);
-}
-
 template <typename T, int D, int RT, int KW, int STAGES, bool FINE>
 __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_attn_q4(const AttnArgs a) {
   typedef _Float16 H;
@@ -301,6 +289,7 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
   if (n <= 0 || group >= tiles) return;
   const int pos0 = max(a.seqs.kv_len[b], 0) - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
   const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
+  if (not_of_this_call(a, b)) return;
   const int m0 = group * ROWS;
   const int p_last = pos0 + (min(m0 + ROWS, pairs) - 1) / g;
   const Blocks blocks = visible_blocks<BT>(pos0 + m0 / g, p_last, kv_len, a.window, a.sinks);
@@ -340,8 +329,7 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
     if (!HALF) {
       top = max(top, (unsigned)__shfl_xor((int)top, 16));
       top = max(top, (unsigned)__shfl_xor((int)top, 32));
-      const int e = max((int)(top >> 7), 1) - 127;
-      if (top != 0 && top < 0x7F80u) shift_q[r] = 10 - e;
+      shift_q[r] = shift_to_half(top);
 #pragma unroll
       for (int x = 0; x < KS; ++x) qf[r][x] = scaled_to_half(qf[r][x], shift_q[r]);
     }
@@ -765,8 +753,8 @@ size_t attn_q4_partial_bytes(const vqv_cache_q4& c, const vqv_seqs& s, int heads
 
 hipError_t launch_paged_attn_q4(const void* q, int dtype, const vqv_cache_q4& c, int layer,
                                 const vqv_seqs& seqs, int heads, float scale, int window,
-                                int sinks, void* out, void* workspace, const AttnPlan& plan,
-                                hipStream_t stream) {
+                                int sinks, int copied_len, void* out, void* workspace,
+                                const AttnPlan& plan, hipStream_t stream) {
   AttnArgs a = attn_args(q, out, seqs, c.page_size, c.pages, c.kv_heads, heads, c.dim, scale,
                          window, sinks, workspace, plan);
   a.k = static_cast<const char*>(c.k) + layer * c.layer_stride;
@@ -774,6 +762,8 @@ hipError_t launch_paged_attn_q4(const void* q, int dtype, const vqv_cache_q4& c,
   a.page_units = (unsigned)(c.page_stride >> 4);
   a.slot_units = (unsigned)(c.slot_stride >> 4);
   a.head_units = (unsigned)(c.head_stride >> 4);
+  if (copied_len > 0) a.which = kOthers;
+  a.copied_len = copied_len;
   const bool few = pairs_of(seqs, heads, c.kv_heads) <= 64;
   return dtype == VQV_BF16 ? launch_type<__bf16>(a, c.dim, plan, few, stream)
                            : launch_type<_Float16>(a, c.dim, plan, few, stream);

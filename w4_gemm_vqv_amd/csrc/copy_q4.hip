@@ -1,0 +1,183 @@
+// A 4-bit cache's tokens as fp16, for calls of many query rows a sequence
+// (vqv_paged_attn_q4).
+//
+// Attention over the records forms every key and value from its code once per
+// tile of 32 (row, head) pairs. From kCopiedPairs pairs on it costs less to form
+// them once, into the workspace, and let the 16-bit cache's attention read them,
+// whose tiles have 256 pairs: 2048 rows over 10240 tokens, 32 heads of 128 on 8, take
+// 412 us, from the records 710 (heads of 256 1226 and 1982).
+// The copy has pages of the cache's size, [page][head][slot][dim], and a table of
+// its own; a page that is not there is not there in the copy either. Sequences of
+// fewer rows, or longer than max_kv says, are read from the records.
+//
+// A sequence's place in the copy is its number or, where rows leave fewer that can
+// be copied, floor(first pair / kCopiedPairs): those that are copied have
+// kCopiedPairs or more each, so no two get the same one.
+
+#include "attn_common.h"
+#include "round_common.h"
+#include "serve_internal.h"
+
+namespace vqv {
+namespace {
+
+constexpr int kTokens = 16;              // of a work-group
+constexpr size_t kMostBytes = 1u << 30;  // of a copy; larger calls read the records
+
+// Scores (rows * heads * tokens of the longest sequence) from which the copy pays
+// for itself and two more launches, with 32 heads of 128 on 8: at 2^27 114 us become
+// 88 (2048 rows of as many tokens) and 226 become 149 (128 of 32768); at 2^26 84
+// would become 128 (1024 of 2048), 96 100 (512 of 4096), but 124 92 (128 of 16384).
+constexpr double kLeastScores = 1 << 27;
+
+struct CopyArgs {
+  const char* k;  // of the layer
+  const char* v;
+  int64_t page_stride, slot_stride, head_stride;
+  int pages, page_size, kv_heads, group;
+  vqv_seqs seqs;
+  int copied_len, width, chunks;
+  bool by_number;  // a sequence's place is its number
+  uint16_t* kc;
+  uint16_t* vc;
+  int32_t* table;
+};
+
+constexpr int threads(int dim) { return (kTokens * dim / 8 + 63) / 64 * 64; }  // whole waves
+
+// One thread per 8 values of a token's head, over all heads. Bound by memory: it
+// reads 80 bytes and writes 256 of each head of 128 values.
+template <int D>
+__global__ __launch_bounds__(threads(D)) void copy_q4(const CopyArgs a) {
+  constexpr int PER = D / 8;
+  typedef __attribute__((ext_vector_type(2))) _Float16 h2;
+  const int slot = blockIdx.x / a.chunks;
+  int b = slot;
+  if (!a.by_number) {
+    // A copied sequence whose first pair is in the slot's range has the range's
+    // last row too.
+    const int row = ((slot + 1) * kCopiedPairs + a.group - 1) / a.group - 1;
+    b = seq_of_row(a.seqs.row_start, a.seqs.n_seqs, row);
+    if (b >= a.seqs.n_seqs || max(a.seqs.row_start[b], 0) * a.group / kCopiedPairs != slot) return;
+  }
+  if (!is_copied(a.seqs, b, a.group, a.copied_len)) return;
+
+  const int t = (blockIdx.x % a.chunks) * kTokens + threadIdx.x / PER, piece = threadIdx.x % PER;
+  const int i = t / a.page_size, s = t % a.page_size;
+  if (threadIdx.x >= kTokens * PER || i >= a.width) return;
+  const int entry = a.seqs.table[b * a.seqs.table_stride + i];
+  const bool there = entry >= 0 && entry < a.pages;
+  if (s == 0 && piece == 0)
+    a.table[(int64_t)b * a.width + i] = there ? slot * a.width + i : -1;
+  if (!there || t >= a.seqs.kv_len[b]) return;
+
+  const int64_t from = entry * a.page_stride + s * a.slot_stride;
+  const int64_t to =
+      ((int64_t)(slot * a.width + i) * a.kv_heads * a.page_size + s) * D + 8 * piece;
+#pragma unroll 4
+  for (int h = 0; h < a.kv_heads; ++h) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const char* rec = (x == 0 ? a.k : a.v) + from + h * a.head_stride;
+      const unsigned codes = *reinterpret_cast<const unsigned*>(rec + 4 * piece);
+      const h2 sb = *reinterpret_cast<const h2*>(rec + D / 2 + piece / 4 * 4);
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack2<_Float16>(
+            fmaf((float)(codes >> (4 * e) & 15u), (float)sb[0], (float)sb[1]),
+            fmaf((float)(codes >> (16 + 4 * e) & 15u), (float)sb[0], (float)sb[1]));
+      *reinterpret_cast<u32x4*>((x == 0 ? a.kc : a.vc) + to + (int64_t)h * a.page_size * D) = w;
+    }
+  }
+}
+
+template <int D>
+hipError_t launch_dim(const CopyArgs& a, int slots, hipStream_t stream) {
+  hipLaunchKernelGGL((copy_q4<D>), dim3((unsigned)(slots * a.chunks)), dim3(threads(D)), 0,
+                     stream, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+CopyPlan copy_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int window) {
+  CopyPlan p = {};
+  const int group = heads / c.kv_heads;
+  const int rows = s.max_rows < s.n_rows ? s.max_rows : s.n_rows;
+  if (window > 0 || (int64_t)rows * group < kCopiedPairs) return p;
+  if ((double)rows * heads * s.max_kv < kLeastScores || s.table_width < 1) return p;
+  const int64_t most = (int64_t)s.n_rows * group / kCopiedPairs;
+  const int64_t slots = most < s.n_seqs ? most : s.n_seqs;
+  int64_t width = ((int64_t)s.max_kv + c.page_size - 1) / c.page_size;
+  if (width > s.table_width) width = s.table_width;
+  const double values = (double)slots * width * c.page_size * c.kv_heads * c.dim * 2;
+  const double table = (double)s.n_seqs * width * 4;
+  if (2 * values + table > (double)kMostBytes) return p;
+  p.width = (int)width;
+  p.slots = (int)slots;
+  p.values = (size_t)values;
+  p.table = ((size_t)table + 15) / 16 * 16;
+  p.attn = attn_plan(copy_cache(c, p, nullptr), copy_seqs(s, p, nullptr), heads, 0, 0);
+  if ((int64_t)c.kv_heads * s.n_seqs * p.attn.groups * p.attn.splits >= (1ll << 23) ||
+      (p.attn.splits > 1 && (int64_t)s.n_rows * heads >= (1ll << 24)))
+    return CopyPlan{};
+  return p;
+}
+
+vqv_cache copy_cache(const vqv_cache_q4& c, const CopyPlan& p, void* workspace) {
+  vqv_cache r = {};
+  r.k = workspace;
+  r.v = static_cast<char*>(workspace) + p.values;
+  r.dtype = VQV_FP16;
+  r.layers = 1;
+  r.pages = p.slots * p.width;
+  r.page_size = c.page_size;
+  r.kv_heads = c.kv_heads;
+  r.dim = c.dim;
+  r.slot_stride = c.dim;
+  r.head_stride = (int64_t)c.page_size * c.dim;
+  r.page_stride = c.kv_heads * r.head_stride;
+  r.layer_stride = r.pages * r.page_stride;
+  return r;
+}
+
+vqv_seqs copy_seqs(const vqv_seqs& s, const CopyPlan& p, void* workspace) {
+  vqv_seqs r = s;
+  r.table = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + 2 * p.values);
+  r.table_stride = p.width;
+  r.table_width = p.width;
+  return r;
+}
+
+hipError_t launch_copy_q4(const vqv_cache_q4& c, int layer, const vqv_seqs& s, int heads,
+                          const CopyPlan& p, void* workspace, hipStream_t stream) {
+  const int64_t tokens = (int64_t)p.width * c.page_size;
+  const CopyArgs a{static_cast<const char*>(c.k) + layer * c.layer_stride,
+                   static_cast<const char*>(c.v) + layer * c.layer_stride,
+                   c.page_stride,
+                   c.slot_stride,
+                   c.head_stride,
+                   c.pages,
+                   c.page_size,
+                   c.kv_heads,
+                   heads / c.kv_heads,
+                   s,
+                   s.max_kv,
+                   p.width,
+                   ceil_div(tokens < s.max_kv ? tokens : s.max_kv, kTokens),
+                   p.slots == s.n_seqs,
+                   static_cast<uint16_t*>(workspace),
+                   reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + p.values),
+                   reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + 2 * p.values)};
+  switch (c.dim) {
+    case 64: return launch_dim<64>(a, p.slots, stream);
+    case 80: return launch_dim<80>(a, p.slots, stream);
+    case 96: return launch_dim<96>(a, p.slots, stream);
+    case 128: return launch_dim<128>(a, p.slots, stream);
+    case 192: return launch_dim<192>(a, p.slots, stream);
+    default: return launch_dim<256>(a, p.slots, stream);
+  }
+}
+
+}  // namespace vqv

@@ -221,9 +221,12 @@ __global__ __launch_bounds__(kThreads) void cache_q4_read(const ReadArgs a) {
       typedef __attribute__((ext_vector_type(2))) _Float16 h2;
       const h2 sb = *reinterpret_cast<const h2*>(rec + D / 2 + piece / 4 * 4);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        w.v[e] = (T)fmaf((float)(codes >> (16 * (e & 1) + 4 * (e >> 1)) & 15u), (float)sb[0],
-                         (float)sb[1]);
+      for (int e = 0; e < 8; ++e) {
+        float x = fmaf((float)(codes >> (16 * (e & 1) + 4 * (e >> 1)) & 15u), (float)sb[0],
+                       (float)sb[1]);
+        asm("" : "+v"(x));  // rounded to fp32: an fp16 product and sum in one would not be
+        w.v[e] = (T)x;
+      }
     }
     *reinterpret_cast<Vec8<T>*>(out + ((int64_t)r * hk + hh) * D + 8 * piece) = w;
   }

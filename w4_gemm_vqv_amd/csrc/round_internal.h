@@ -39,6 +39,12 @@ hipError_t launch_paged_attn(const void* q, const vqv_cache& cache, int layer,
                              void* out, void* workspace, const AttnPlan& plan,
                              hipStream_t stream);
 
+// bf16 queries and outputs over an fp16 cache, of the sequences that are copied to
+// it, without a window; plans with mw of 4 or 8.
+hipError_t launch_paged_attn_copied(const void* q, const vqv_cache& cache, const vqv_seqs& seqs,
+                                    int heads, float scale, int copied_len, void* out,
+                                    void* workspace, const AttnPlan& plan, hipStream_t stream);
+
 hipError_t launch_cache_copy(const vqv_cache& cache, const int32_t* src, const int32_t* dst,
                              int n, hipStream_t stream);
 hipError_t launch_cache_trim(const vqv_pages& pages, const int32_t* keep_len, const int32_t* rows,

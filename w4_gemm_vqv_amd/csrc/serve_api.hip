@@ -117,7 +117,7 @@ namespace {
 
 // What vqv_paged_attn_q4 checks of its sizes, and the plan.
 vqv_status plan_attn_q4(const vqv_cache_q4* cache, const vqv_seqs* seqs, int heads, int window,
-                        int sinks, vqv::AttnPlan* plan) {
+                        int sinks, vqv::AttnPlan* plan, vqv::CopyPlan* copy) {
   vqv_status st = check_cache_q4(cache);
   if (st != VQV_OK) return st;
   if ((st = check_seqs(seqs)) != VQV_OK) return st;
@@ -130,7 +130,20 @@ vqv_status plan_attn_q4(const vqv_cache_q4* cache, const vqv_seqs* seqs, int hea
   if ((int64_t)cache->kv_heads * seqs->n_seqs * plan->groups * plan->splits >= (1ll << 23))
     return VQV_ERR_UNSUPPORTED;  // threads of a grid are counted in 32 bits
   if (plan->splits > 1 && (int64_t)seqs->n_rows * heads >= (1ll << 24)) return VQV_ERR_UNSUPPORTED;
+  *copy = vqv::copy_plan(*cache, *seqs, heads, window);
   return VQV_OK;
+}
+
+// Of the partial sums over the records, and, where tokens are copied, of the copy
+// and the sums over it (at the workspace's start, in turn).
+size_t attn_q4_bytes(const vqv_cache_q4& cache, const vqv_seqs& seqs, int heads,
+                     const vqv::AttnPlan& plan, const vqv::CopyPlan& copy) {
+  size_t part = vqv::attn_q4_partial_bytes(cache, seqs, heads, plan);
+  if (copy.slots == 0) return part;
+  const size_t wide =
+      vqv::attn_partial_bytes(vqv::copy_cache(cache, copy, nullptr), seqs, heads, copy.attn);
+  if (wide > part) part = wide;
+  return (part + 15) / 16 * 16 + copy.bytes();
 }
 
 }  // namespace
@@ -140,8 +153,9 @@ extern "C" {
 size_t vqv_paged_attn_q4_workspace_bytes(const vqv_cache_q4* cache, const vqv_seqs* seqs,
                                          int heads, int window, int sinks) {
   vqv::AttnPlan plan;
-  if (plan_attn_q4(cache, seqs, heads, window, sinks, &plan) != VQV_OK) return 0;
-  return vqv::attn_q4_partial_bytes(*cache, *seqs, heads, plan);
+  vqv::CopyPlan copy;
+  if (plan_attn_q4(cache, seqs, heads, window, sinks, &plan, &copy) != VQV_OK) return 0;
+  return attn_q4_bytes(*cache, *seqs, heads, plan, copy);
 }
 
 vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4* cache, int layer,
@@ -149,7 +163,8 @@ vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4*
                              void* out, void* workspace, size_t workspace_bytes,
                              void* hip_stream) {
   vqv::AttnPlan plan;
-  const vqv_status st = plan_attn_q4(cache, seqs, heads, window, sinks, &plan);
+  vqv::CopyPlan copy;
+  const vqv_status st = plan_attn_q4(cache, seqs, heads, window, sinks, &plan, &copy);
   if (st != VQV_OK) return st;
   if ((seqs->n_rows && (!q || !out)) || layer < 0 || layer >= cache->layers) return VQV_ERR_ARG;
   if (dtype == VQV_FP32) return VQV_ERR_UNSUPPORTED;
@@ -157,7 +172,9 @@ vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4*
   if (!(scale > 0.0f) || !isfinite(scale)) return VQV_ERR_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return VQV_ERR_ALIGN;
   const size_t bytes = (size_t)seqs->n_rows * heads * cache->dim * 2;
-  const size_t need = vqv::attn_q4_partial_bytes(*cache, *seqs, heads, plan);
+  // fp16 keys as one value each would be the larger part of fp16 outputs' error.
+  if (dtype != VQV_BF16) copy = {};
+  const size_t need = attn_q4_bytes(*cache, *seqs, heads, plan, copy);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return VQV_ERR_WORKSPACE;
   if (overlaps(out, bytes, q, bytes) || overlaps(workspace, need, q, bytes) ||
@@ -165,9 +182,19 @@ vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4*
     return VQV_ERR_ARG;
   if (seqs->n_rows == 0 || seqs->max_rows == 0) return VQV_OK;
   (void)hipGetLastError();
+  const auto stream = static_cast<hipStream_t>(hip_stream);
+  if (copy.slots) {
+    void* held = static_cast<char*>(workspace) + (need - copy.bytes());
+    hipError_t e = vqv::launch_copy_q4(*cache, layer, *seqs, heads, copy, held, stream);
+    if (e == hipSuccess)
+      e = vqv::launch_paged_attn_copied(q, vqv::copy_cache(*cache, copy, held),
+                                        vqv::copy_seqs(*seqs, copy, held), heads, scale,
+                                        seqs->max_kv, out, workspace, copy.attn, stream);
+    if (e != hipSuccess) return status_of(e);
+  }
   return status_of(vqv::launch_paged_attn_q4(q, (int)dtype, *cache, layer, *seqs, heads, scale,
-                                             window, sinks, out, workspace, plan,
-                                             static_cast<hipStream_t>(hip_stream)));
+                                             window, sinks, copy.slots ? seqs->max_kv : 0, out,
+                                             workspace, plan, stream));
 }
 
 }  // extern "C"
