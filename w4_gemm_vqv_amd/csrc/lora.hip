@@ -14,6 +14,12 @@
 //
 // Weights are the A operand of both products, so that a lane ends with four
 // neighbouring ranks (columns) of one row and moves them as 16 bytes.
+//
+// What bounds it, y not in a cache: 2100 rows of three adapters of rank 64, 5120 to
+// 17408 columns in fp16, take 115 us, 19 of them in the first kernel, for 320 MB
+// (2.8 TB/s; y and out are 292 MB of it); 64 rows of 40 adapters of rank 32, 2560 to
+// 18432, 19 us for 51 MB (2.6 TB/s); 8 rows of rank 16 10.5 us, which are two
+// launches and three waits for memory, one after the other, in each.
 
 #include "serve_internal.h"
 
@@ -355,6 +361,47 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
   const bool real = m < count;
   const int64_t row = block * kBlock + nth_row(s.rows, real ? m : 0);
 
+  const uint16_t* w = static_cast<const uint16_t*>(a.ad.b) + (int64_t)s.adapter * N * a.ad.rank;
+  const unsigned wl = lds_offset(staged[wave]);
+  float* sums = reinterpret_cast<float*>(staged[wave] + COLS * RB * 64);
+  const int pieces = a.ad.rank / 8;
+  // Pieces of the staged weights: place p has piece `from` of them, in bytes.
+  // p / pieces = p * mul >> 16 for p below 2048.
+  constexpr int LOADS = CT * RB;
+  const int mul = (65535 + pieces) / pieces;
+  int from[LOADS];
+#pragma unroll
+  for (int e = 0; e < LOADS; ++e) {
+    const int p = min(e * 64 + lane, COLS * pieces - 1), r = p * mul >> 16, c = p - r * pieces;
+    from[e] = (r * pieces + piece_of(pieces, r, c)) * 16;
+  }
+  // This lane's rows of y and out, and its 4 columns of them: a row to 4 CT lanes.
+  const int of_row = lane / (4 * CT), of_col = lane % (4 * CT) * 4;
+  int64_t rows[CT];
+#pragma unroll
+  for (int i = 0; i < CT; ++i) {
+    const int r = 16 / CT * i + of_row;
+    rows[i] = (int64_t)block * kBlock + __shfl((int)(row - (int64_t)block * kBlock), r);
+  }
+  const int step = tiles == 1 ? COLS * kExpandWaves : COLS;
+  int n0 = c0 + (tiles == 1 ? COLS * wave : 0);
+  // The weights and y of the next COLS columns are asked for while the last sums are
+  // stored, the first while the row's values are formed (asked for as they are needed:
+  // 150 us instead of 120 for 2100 rows of rank 64, y not in a cache).
+  F4 v[CT];
+  const auto ask = [&](int n0) {
+    // COLS rows of weights, as they lie.
+    const char* rows_at = reinterpret_cast<const char*>(w + (int64_t)n0 * a.ad.rank);
+#pragma unroll
+    for (int e = 0; e < LOADS; ++e)
+      if (e * 64 < COLS * pieces)
+        load16_to_lds(rows_at + from[e], __builtin_amdgcn_readfirstlane(wl + e * 1024));
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+      __builtin_memcpy(&v[i], a.y + rows[i] * a.y_stride + n0 + of_col, 16);
+  };
+  if (n0 + COLS <= end) ask(n0);
+
   // The row's values between the products, as B operands.
   s16x8 low[RB][3];
   float back = scale;
@@ -414,7 +461,6 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
       }
   }
 
-  const uint16_t* w = static_cast<const uint16_t*>(a.ad.b) + (int64_t)s.adapter * N * a.ad.rank;
   const auto product = [&](s16x8* wf) {
     // Weights past the rank are not used, whatever they are.
     if (rank != 32 * RB) {
@@ -432,43 +478,10 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
     return acc;
   };
 
-  const unsigned wl = lds_offset(staged[wave]);
-  float* sums = reinterpret_cast<float*>(staged[wave] + COLS * RB * 64);
-  const int pieces = a.ad.rank / 8;
-  // Pieces of the staged weights: place p has piece `from` of them, in bytes.
-  // p / pieces = p * mul >> 16 for p below 2048.
-  constexpr int LOADS = CT * RB;
-  const int mul = (65535 + pieces) / pieces;
-  int from[LOADS];
-#pragma unroll
-  for (int e = 0; e < LOADS; ++e) {
-    const int p = min(e * 64 + lane, COLS * pieces - 1), r = p * mul >> 16, c = p - r * pieces;
-    from[e] = (r * pieces + piece_of(pieces, r, c)) * 16;
-  }
-  // This lane's rows of y and out, and its 4 columns of them: a row to 4 CT lanes.
-  const int of_row = lane / (4 * CT), of_col = lane % (4 * CT) * 4;
-  int64_t rows[CT];
   float by[CT];
 #pragma unroll
-  for (int i = 0; i < CT; ++i) {
-    const int r = 16 / CT * i + of_row;
-    rows[i] = (int64_t)block * kBlock + __shfl((int)(row - (int64_t)block * kBlock), r);
-    by[i] = __shfl(back, r);
-  }
-  const int step = tiles == 1 ? COLS * kExpandWaves : COLS;
-  int n0 = c0 + (tiles == 1 ? COLS * wave : 0);
+  for (int i = 0; i < CT; ++i) by[i] = __shfl(back, 16 / CT * i + of_row);
   for (; n0 + COLS <= end; n0 += step) {
-    // COLS rows of weights, as they lie.
-    const char* rows_at = reinterpret_cast<const char*>(w + (int64_t)n0 * a.ad.rank);
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the last reads are done
-#pragma unroll
-    for (int e = 0; e < LOADS; ++e)
-      if (e * 64 < COLS * pieces)
-        load16_to_lds(rows_at + from[e], __builtin_amdgcn_readfirstlane(wl + e * 1024));
-    F4 v[CT];
-#pragma unroll
-    for (int i = 0; i < CT; ++i)
-      __builtin_memcpy(&v[i], a.y + rows[i] * a.y_stride + n0 + of_col, 16);
     loaded();
 #pragma unroll
     for (int t = 0; t < CT; ++t) {
@@ -482,14 +495,18 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
       const f32x4 acc = product(wf);
       *reinterpret_cast<f32x4*>(sums + col * (COLS + 4) + 16 * t + 4 * quarter) = acc;
     }
-    asm volatile("" ::: "memory");
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the weights are read
+    F4 old[CT];
+#pragma unroll
+    for (int i = 0; i < CT; ++i) old[i] = v[i];
+    if (n0 + step + COLS <= end) ask(n0 + step);
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
       const int m = 16 / CT * i + of_row;
       const f32x4 acc = *reinterpret_cast<const f32x4*>(sums + m * (COLS + 4) + of_col);
       f32x4 r;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = fmaf(acc[e], by[i], v[i].v[e]);
+      for (int e = 0; e < 4; ++e) r[e] = fmaf(acc[e], by[i], old[i].v[e]);
       // Written once and not read again here: past the L2, which holds weights.
       if (tile * 16 + m < count) {
         typedef __attribute__((ext_vector_type(4), aligned(4))) float f32x4_4;
@@ -541,12 +558,13 @@ Plan plan_of(const vqv_adapters& ad, int M) {
   if (splits > steps / 16) splits = steps / 16;
   if (splits > 8) splits = 8;
   p.splits = splits < 1 ? 1 : splits;
-  // Columns of a work-group of the second kernel: 64 to a wave, or 16 where that
-  // leaves fewer than one work-group to a CU if an eighth of the slots are taken,
-  // or the weights of 64 would take all of a CU's LDS.
+  // Columns of a work-group of the second kernel: 128 to a wave, 64 at a time (2100
+  // rows, rank 64: 115 us, with 64 120, with 256 132; 64 rows of 40 adapters of rank
+  // 32: 19.3, 21.5, 23.7), or 16 where 64 leave fewer than one work-group to a CU if
+  // an eighth of the slots are taken, or the weights of 64 would take all of a CU's LDS.
   const int64_t some = (int64_t)p.blocks * (p.slots / 8 > 1 ? p.slots / 8 : 1);
   const bool few = ad.rank > 128 || some * ceil_div(ad.N, 64 * kExpandWaves) < 256;
-  p.cols = kExpandWaves * (few ? 16 : 64);
+  p.cols = kExpandWaves * (few ? 16 : 128);
   p.col_groups = ceil_div(ad.N, p.cols);
   return p;
 }
@@ -579,7 +597,7 @@ hipError_t expand(const LoraArgs& a, const Plan& p, hipStream_t stream) {
 template <typename T, int RB>
 hipError_t expand_cols(const LoraArgs& a, const Plan& p, hipStream_t stream) {
   if constexpr (RB < 8) {
-    if (p.cols == 64 * kExpandWaves) return expand<T, RB, 4>(a, p, stream);
+    if (p.cols == 128 * kExpandWaves) return expand<T, RB, 4>(a, p, stream);
   }
   return expand<T, RB, 1>(a, p, stream);
 }

@@ -16,7 +16,7 @@
 // does not depend on timing.
 //
 // What bounds it: a 64-bit exponential is about 25 instructions at half the rate
-// of fp32 or less, so the first kernel takes 8 us for 16 x 4 rows of 152064 logits
+// of fp32 or less, so the first kernel takes 8 us for 16 x 4 rows of 151936 logits
 // (39 MB: 4.9 TB/s) and 13 us for 64 rows where every row has a temperature of its
 // own, and the second, three passes over a row's chunks with a wait for the last
 // work-group between, 7 to 10.5. Together (1 x 8, 4 x 16 with draft
