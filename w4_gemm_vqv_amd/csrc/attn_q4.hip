@@ -1,25 +1,41 @@
 // Attention of new rows over a paged cache held in 4 bits (vqv_paged_attn_q4).
 //
 // As in attn.hip, the (row, head) pairs of a sequence that share a key head are
-// cut into tiles of 32, S^T = K Q^T and O^T = V^T P^T are formed with 32x32x16
-// matrix instructions and a running maximum, and long sequences are split over
-// work-groups whose sums a second kernel joins. What differs is how keys and
-// values come: records of 4-bit codes with a scale and a bias per 32 values
-// (a token's record of 128 values is 80 bytes instead of 256).
+// cut into tiles, S^T = K Q^T and O^T = V^T P^T are formed with matrix
+// instructions (here 16x16x32 in fp16) and a running maximum, and long sequences
+// are split over work-groups whose sums a second kernel joins. What differs is how
+// keys and values come: records of 4-bit codes with a scale and a bias per 32
+// values (a token's record of 128 values is 80 bytes instead of 256).
 //
 // Each wave walks over its own blocks of 32 tokens, every KW-th one of the
-// work-group's, for RT tiles of rows: it loads their records to an LDS buffer
-// of its own, STAGES deep, and waits for nobody else. A lane takes half of
-// token l % 32's record: its keys become fp16 in registers, right where the A
-// operand wants them (a matrix step's 16 columns are 8 of each lane half's
-// group, and the query rows are read in that order), its values become fp16 in
-// LDS, where the transposing read turns them.
+// work-group's, for RT tiles of 16 rows: it copies their records to LDS as they
+// are, two blocks deep, and waits for nobody else; a token's page is looked up
+// three blocks ahead. Keys: a lane's codes become fp16 right where the A operand
+// wants them (a matrix step's 32 columns are chunks of 8 codes that lie together,
+// and the query rows are read in that order). Values: the transposing read of 4-bit
+// elements gives a lane one column's codes of 16 tokens, that of 16-bit elements
+// their scales and biases, so nothing but codes is moved. (Values made fp16 first,
+// written to LDS and read transposed: 229 us for decode instead of 164.)
 //
 // A code becomes fp16 by placing it under an exponent (1024 + q, or 64 + q for
 // those that stand 4 bits higher: no shift), subtracting that, which is exact,
 // and one fused multiply-add: 13 instructions for 8 values, and a single
 // rounding, 2^-12 of a value. bf16 queries become fp16 times a power of two per
-// row, exact but for values 2^24 below the row's largest.
+// row, exact but for values 2^24 below the row's largest. Keys of fp16 queries
+// stay in two fp16 values: rounded once, they would make the larger part of an
+// fp16 output's error.
+//
+// All work-groups of a sequence's tokens run on one XCD whatever their key head:
+// with slots as the outer order the records of neighbouring heads share cache
+// lines (decode 229 us without that, 175 with).
+//
+// What bounds it, with 32 heads of 128 on 8 (a copy moves 4.8 TB/s here):
+//   48 ragged sequences to 16383 tokens, one row each: 164 us for 565 MB, 3.4 TB/s:
+//   the records' loads; the 16-bit cache takes 349 us for 1.8 GB.
+//   8 rows over 4096 tokens: 15 us, two launches and a chain of waits, for 5 MB.
+//   16 sequences of 16 rows, 16 heads of 256 on 4 in fp16, a window of 4096: 125 us
+//   for 86 MB: forming keys in two values and weights in one for two tiles of rows.
+// Large bf16 calls without a window go through copy_q4.hip instead.
 
 #include "attn_common.h"
 #include "serve_internal.h"
@@ -255,7 +271,8 @@ __device__ __forceinline__ float max_of_quarters(float x) {
 }
 
 template <typename T, int D, int RT, int KW, int STAGES, bool FINE>
-__global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_attn_q4(const AttnArgs a) {
+__global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_attn_q4(
+    const AttnArgs a) {
   typedef _Float16 H;
   constexpr bool HALF = Bits<T>::exponent == Bits<H>::exponent;  // fp16 queries and outputs
   constexpr int BT = KW * 32, DT = D / 16, KS = Keys<D>::STEPS, VG = Values<D>::GROUPS;
