@@ -15,13 +15,11 @@
 // between two tokens in a few of a hundred draws. Sums are taken in an order that
 // does not depend on timing.
 //
-// What bounds it: a 64-bit exponential is about 25 instructions at half the rate
-// of fp32 or less, so the first kernel takes 8 us for 16 x 4 rows of 151936 logits
-// (39 MB: 4.9 TB/s) and 13 us for 64 rows where every row has a temperature of its
-// own, and the second, three passes over a row's chunks with a wait for the last
-// work-group between, 7 to 10.5. Together (1 x 8, 4 x 16 with draft
-// probabilities, 64 x 1): 15, 19 and 19 us. With one work-group's atomic sums in
-// LDS and 256 threads a draw it was 31, 37 and 35.
+// What bounds it: the 64-bit exponentials beside the loads in the first kernel (64
+// rows of 151936 logits: 13 us, 3 TB/s); the second is a chain of passes over a
+// row's chunks, with a wait for the last work-group between, of 7 to 10.5 us.
+// Together, for 1 x 8 and 4 x 16 rows with draft probabilities and 64 x 1: 15, 19
+// and 19 us. With sums by LDS atomics and 256 threads a draw: 31, 37 and 35.
 
 #include <limits.h>
 
