@@ -5,7 +5,7 @@
 // tile of 32 (row, head) pairs. From kCopiedPairs pairs on it costs less to form
 // them once, into the workspace, and let the 16-bit cache's attention read them,
 // whose tiles have 256 pairs: 2048 rows over 10240 tokens, 32 heads of 128 on 8, take
-// 412 us, from the records 710 (heads of 256 1226 and 1982).
+// 393 us, from the records 710 (heads of 256 1226 and 1982).
 // The copy has pages of the cache's size, [page][head][slot][dim], and a table of
 // its own; a page that is not there is not there in the copy either. Sequences of
 // fewer rows, or longer than max_kv says, are read from the records.
@@ -45,13 +45,15 @@ struct CopyArgs {
 
 constexpr int threads(int dim) { return (kTokens * dim / 8 + 63) / 64 * 64; }  // whole waves
 
-// One thread per 8 values of a token's head, over all heads. Bound by memory: it
-// reads 80 bytes and writes 256 of each head of 128 values.
+// One thread per 8 values of a token's key and value head, a work-group per head:
+// 10240 tokens of 8 heads of 128 in 12.5 us, 55 MB at 4.4 TB/s (two heads to a
+// work-group 14.5, all eight 21).
 template <int D>
 __global__ __launch_bounds__(threads(D)) void copy_q4(const CopyArgs a) {
   constexpr int PER = D / 8;
   typedef __attribute__((ext_vector_type(2))) _Float16 h2;
-  const int slot = blockIdx.x / a.chunks;
+  const int part = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads;
+  const int slot = part / a.chunks;
   int b = slot;
   if (!a.by_number) {
     // A copied sequence whose first pair is in the slot's range has the range's
@@ -62,39 +64,36 @@ __global__ __launch_bounds__(threads(D)) void copy_q4(const CopyArgs a) {
   }
   if (!is_copied(a.seqs, b, a.group, a.copied_len)) return;
 
-  const int t = (blockIdx.x % a.chunks) * kTokens + threadIdx.x / PER, piece = threadIdx.x % PER;
+  const int t = part % a.chunks * kTokens + threadIdx.x / PER, piece = threadIdx.x % PER;
   const int i = t / a.page_size, s = t % a.page_size;
   if (threadIdx.x >= kTokens * PER || i >= a.width) return;
   const int entry = a.seqs.table[b * a.seqs.table_stride + i];
   const bool there = entry >= 0 && entry < a.pages;
-  if (s == 0 && piece == 0)
+  if (s == 0 && piece == 0 && h == 0)
     a.table[(int64_t)b * a.width + i] = there ? slot * a.width + i : -1;
   if (!there || t >= a.seqs.kv_len[b]) return;
 
-  const int64_t from = entry * a.page_stride + s * a.slot_stride;
+  const int64_t from = entry * a.page_stride + s * a.slot_stride + h * a.head_stride;
   const int64_t to =
-      ((int64_t)(slot * a.width + i) * a.kv_heads * a.page_size + s) * D + 8 * piece;
-#pragma unroll 4
-  for (int h = 0; h < a.kv_heads; ++h) {
+      (((int64_t)(slot * a.width + i) * a.kv_heads + h) * a.page_size + s) * D + 8 * piece;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const char* rec = (x == 0 ? a.k : a.v) + from + h * a.head_stride;
-      const unsigned codes = *reinterpret_cast<const unsigned*>(rec + 4 * piece);
-      const h2 sb = *reinterpret_cast<const h2*>(rec + D / 2 + piece / 4 * 4);
-      u32x4 w;
+  for (int x = 0; x < 2; ++x) {
+    const char* rec = (x == 0 ? a.k : a.v) + from;
+    const unsigned codes = *reinterpret_cast<const unsigned*>(rec + 4 * piece);
+    const h2 sb = *reinterpret_cast<const h2*>(rec + D / 2 + piece / 4 * 4);
+    u32x4 w;
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[e] = pack2<_Float16>(
-            fmaf((float)(codes >> (4 * e) & 15u), (float)sb[0], (float)sb[1]),
-            fmaf((float)(codes >> (16 + 4 * e) & 15u), (float)sb[0], (float)sb[1]));
-      *reinterpret_cast<u32x4*>((x == 0 ? a.kc : a.vc) + to + (int64_t)h * a.page_size * D) = w;
-    }
+    for (int e = 0; e < 4; ++e)
+      w[e] =
+          pack2<_Float16>(fmaf((float)(codes >> (4 * e) & 15u), (float)sb[0], (float)sb[1]),
+                          fmaf((float)(codes >> (16 + 4 * e) & 15u), (float)sb[0], (float)sb[1]));
+    *reinterpret_cast<u32x4*>((x == 0 ? a.kc : a.vc) + to) = w;
   }
 }
 
 template <int D>
 hipError_t launch_dim(const CopyArgs& a, int slots, hipStream_t stream) {
-  hipLaunchKernelGGL((copy_q4<D>), dim3((unsigned)(slots * a.chunks)), dim3(threads(D)), 0,
+  hipLaunchKernelGGL((copy_q4<D>), dim3((unsigned)(slots * a.chunks * a.kv_heads)), dim3(threads(D)), 0,
                      stream, a);
   return hipGetLastError();
 }
