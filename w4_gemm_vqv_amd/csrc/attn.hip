@@ -482,25 +482,25 @@ hipError_t launch_type(const AttnArgs& a, int dim, const AttnPlan& p, hipStream_
   }
 }
 
-// bf16 queries over the fp16 copy of a 4-bit cache: plans of many rows alone.
+// bf16 queries over the fp16 copy of a 4-bit cache: only the plans of many rows
+// without a window.
 template <int D>
-hipError_t launch_copied_dim(const AttnArgs& a, const AttnPlan& p, hipStream_t stream) {
+hipError_t launch_copied_dim(const AttnArgs& a, hipStream_t stream) {
   if constexpr (D <= 128) {
-    if (p.mw == 8) return launch_shape<_Float16, D, 8, 1, 64, 4, __bf16>(a, stream);
-    return launch_shape<_Float16, D, 4, 1, 64, 2, __bf16>(a, stream);
+    return launch_shape<_Float16, D, 8, 1, 64, 4, __bf16>(a, stream);
   } else {
     return launch_shape<_Float16, D, 4, 1, 32, 4, __bf16>(a, stream);
   }
 }
 
-hipError_t launch_copied(const AttnArgs& a, int dim, const AttnPlan& p, hipStream_t stream) {
+hipError_t launch_copied(const AttnArgs& a, int dim, hipStream_t stream) {
   switch (dim) {
-    case 64: return launch_copied_dim<64>(a, p, stream);
-    case 80: return launch_copied_dim<80>(a, p, stream);
-    case 96: return launch_copied_dim<96>(a, p, stream);
-    case 128: return launch_copied_dim<128>(a, p, stream);
-    case 192: return launch_copied_dim<192>(a, p, stream);
-    default: return launch_copied_dim<256>(a, p, stream);
+    case 64: return launch_copied_dim<64>(a, stream);
+    case 80: return launch_copied_dim<80>(a, stream);
+    case 96: return launch_copied_dim<96>(a, stream);
+    case 128: return launch_copied_dim<128>(a, stream);
+    case 192: return launch_copied_dim<192>(a, stream);
+    default: return launch_copied_dim<256>(a, stream);
   }
 }
 
@@ -589,7 +589,7 @@ hipError_t launch_paged_attn_copied(const void* q, const vqv_cache& c, const vqv
   AttnArgs a = args_of(q, c, 0, seqs, heads, scale, 0, 0, out, workspace, plan);
   a.which = kCopied;
   a.copied_len = copied_len;
-  return launch_copied(a, c.dim, plan, stream);
+  return launch_copied(a, c.dim, stream);
 }
 
 }  // namespace vqv

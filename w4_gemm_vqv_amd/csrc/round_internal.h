@@ -40,7 +40,7 @@ hipError_t launch_paged_attn(const void* q, const vqv_cache& cache, int layer,
                              hipStream_t stream);
 
 // bf16 queries and outputs over an fp16 cache, of the sequences that are copied to
-// it, without a window; plans with mw of 4 or 8.
+// it, without a window; plans of 512 (row, head) pairs or more.
 hipError_t launch_paged_attn_copied(const void* q, const vqv_cache& cache, const vqv_seqs& seqs,
                                     int heads, float scale, int copied_len, void* out,
                                     void* workspace, const AttnPlan& plan, hipStream_t stream);
