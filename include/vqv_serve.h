@@ -158,7 +158,7 @@ vqv_status vqv_verify_sampled(const float* logits, const int32_t* draft, const f
  * device or NULL (all `rank`): of adapter e the first ranks[e] are used (cut to
  * 0..rank), the others are not read.
  *   rank       a multiple of 8, 8..256; K a multiple of 8, 8 <= K <= 32768;
- *              N >= 1 (else VQV_ERR_ARG or, past the largest,
+ *              1 <= N < 2^31 - 4096 (else VQV_ERR_ARG or, past the largest,
  *              VQV_ERR_UNSUPPORTED).
  */
 typedef struct {

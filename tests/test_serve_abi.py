@@ -250,3 +250,12 @@ def test_lora_grid_limits(S, L):
     ad = adapters(S, n=1000, N=100000)
     assert lora_call(S, L, ad, M=1 << 21, ys=100000, os=100000, wn=1 << 60) == UNSUP
     assert L.vqv_lora_add_workspace_bytes(ad, 1 << 21) == 0
+
+
+@pytest.mark.parametrize("N", [2 ** 31 - 1, 2 ** 31 - 512, 2 ** 31 - 4096])
+def test_lora_columns_past_32_bits(S, L, N):
+    """Columns are counted in 32 bits, past the last one to the end of the work-groups' share."""
+    ad = adapters(S, n=1, rank=8, K=8, N=N)
+    assert lora_call(S, L, ad, M=1, ys=N, os=N, wn=1 << 60) == UNSUP
+    assert L.vqv_lora_add_workspace_bytes(ad, 1) == 0
+    assert L.vqv_lora_add_workspace_bytes(adapters(S, n=1, rank=8, K=8, N=2 ** 31 - 4097), 1) > 0

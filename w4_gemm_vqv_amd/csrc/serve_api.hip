@@ -217,7 +217,9 @@ vqv_status check_adapters(const vqv_adapters* a) {
     return VQV_ERR_ARG;
   if (a->dtype == VQV_FP32) return VQV_ERR_UNSUPPORTED;
   if (!half_type(a->dtype)) return VQV_ERR_ARG;
-  if (a->rank > 256 || a->K > 32768) return VQV_ERR_UNSUPPORTED;
+  // Columns past the last, up to the end of its work-group and of the 8 groups that go to the
+  // XCDs together (lora.hip), are counted in 32 bits.
+  if (a->rank > 256 || a->K > 32768 || a->N > INT32_MAX - 8 * 512) return VQV_ERR_UNSUPPORTED;
   if (!aligned(a->a, 16) || !aligned(a->b, 16) || !words_aligned(a->scale, a->ranks))
     return VQV_ERR_ALIGN;
   return VQV_OK;
