@@ -186,3 +186,19 @@ def test_no_rows_and_refusals(vqv):
         vqv.Adapters(c.a.cuda(), c.b[:, :, :4].contiguous().cuda(), c.scale.cuda())
     with pytest.raises(ValueError):
         vqv.Adapters(c.a.cuda(), c.b.cuda(), c.scale[:1].cuda())
+
+
+@pytest.mark.parametrize("weight", ["bf16", "fp16"])
+def test_infinities_between_the_products(vqv, weight):
+    """One rank's sum is an infinity, which decides the output by its weight's sign; the others are finite, past
+    the weights' type too. Then a finite sum that the weights' type would round to an infinity."""
+    c = Case([0] * 5 + [1] * 40, K=64, N=300, rank=16, n=2, act="fp32", weight=weight, size=1e6)
+    c.x[:, 5] = c.x[:, 5].abs() + 1
+    c.a[:, 3, 5] = float("inf")
+    want, got = c.want()[0], vqv.vqv_lora_add(c.x.cuda(), c.set(vqv), c.which.cuda(), c.y.cuda()).cpu()
+    assert want.isinf().all() and torch.equal(got, want.float())
+    c = Case([0] * 3 + [1] * 30, K=8, N=70, rank=8, n=2, act="fp32", weight=weight)
+    c.x[:], c.a[:] = 0, 0
+    c.x[:, 2], c.a[:, :, 2] = 3.3999e38, 1.0
+    c.b *= 2.0 ** -9
+    c.close(vqv.vqv_lora_add(c.x.cuda(), c.set(vqv), c.which.cuda(), c.y.cuda()), c.want())

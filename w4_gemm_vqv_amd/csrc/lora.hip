@@ -36,6 +36,11 @@ constexpr int kShrinkWaves = 8;
 constexpr int kExpandWaves = 4;
 
 template <typename T>
+constexpr bool kHalf = false;
+template <>
+constexpr bool kHalf<_Float16> = true;
+
+template <typename T>
 __device__ __forceinline__ f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c);
 template <>
 __device__ __forceinline__ f32x4 mfma16<__bf16>(s16x8 a, s16x8 b, f32x4 c) {
@@ -298,15 +303,19 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink(const LoraArgs 
   }
 }
 
-// x in three values of T, which hold all of its bits; an infinity or NaN in one.
+// x in three values of T, which hold all of its bits (in fp16 those down to 2^-24: 2^-38 of a
+// row's largest value); an infinity or NaN in one. Finite values that T would round to an
+// infinity are cut to its largest, and the rest is in the others.
 template <typename T>
 __device__ __forceinline__ void split3(float x, short* out) {
+  constexpr float most = kHalf<T> ? 65504.0f : 0x1.FEp127f;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const T t = (T)x;
+    const bool real = fabsf(x) < __builtin_inff();
+    const T t = (T)(real ? fminf(fmaxf(x, -most), most) : x);
     out[i] = __builtin_bit_cast(short, t);
     const float rest = x - (float)t;
-    x = fabsf(x) < __builtin_inff() ? rest : 0.0f;
+    x = real ? rest : 0.0f;
   }
 }
 
@@ -436,14 +445,15 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (r + e >= rank) v[i][e] = 0.0f;
-        top = fmaxf(top, fabsf(v[i][e]));
+        const float size = fabsf(v[i][e]);
+        if (size < __builtin_inff()) top = fmaxf(top, size);
       }
     }
-    if (sizeof(T) == 2 && __builtin_bit_cast(unsigned short, (T)1.0f) == 0x3C00) {
-      // fp16: the row times a power of two, its largest value near 2^14.
+    if (kHalf<T>) {
+      // fp16: the row times a power of two, its largest finite value near 2^14.
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
-      const int e = top > 0.0f && top < __builtin_inff() ? 14 - (int)ilogbf(top) : 0;
+      const int e = top > 0.0f ? 14 - (int)ilogbf(top) : 0;
 #pragma unroll
       for (int i = 0; i < RB; ++i)
 #pragma unroll
