@@ -202,3 +202,50 @@ def test_infinities_between_the_products(vqv, weight):
     c.x[:, 2], c.a[:, :, 2] = 3.3999e38, 1.0
     c.b *= 2.0 ** -9
     c.close(vqv.vqv_lora_add(c.x.cuda(), c.set(vqv), c.which.cuda(), c.y.cuda()), c.want())
+
+
+# Calls whose second kernel takes 64 columns at a time: ranks of up to 128, and enough columns and slots.
+WIDE = [
+    dict(which=[i * 7 % 66 - 1 for i in range(64)], K=72, N=8203, rank=8, n=64),
+    dict(which=[i * 5 % 64 for i in range(64)], K=136, N=8450, rank=24, n=64, act="fp16"),
+    dict(which=[0] * 70 + [-1] * 3 + [1, 2] * 50 + [2] * 127, K=264, N=13999, rank=64, n=3),
+    dict(which=[i % 4 - 1 for i in range(300)], K=64, N=13121, rank=96, n=3, act="fp16"),
+    dict(which=[i // 101 for i in range(300)], K=200, N=13500, rank=128, n=3),
+    dict(which=[2] * 60 + [0, 1] * 20 + [1] * 199, K=64, N=13315, rank=40, n=3, act="fp32", weight="fp16"),
+    dict(which=[1, 0, 3] * 100, K=96, N=13077, rank=128, n=2, act="fp32"),
+    dict(which=[0] * 64, K=64, N=65601, rank=16, n=1, act="fp16"),
+]
+
+
+def is_wide(c):
+    M, n, N = len(c["which"]), c["n"], c["N"]
+    slots = min(n, 64, M)
+    return c["rank"] <= 128 and -(-M // 64) * max(slots // 8, 1) * -(-N // 256) >= 256
+
+
+@pytest.mark.parametrize("case", WIDE, ids=lambda c: f"{len(c['which'])}x{c['K']}x{c['N']}r{c['rank']}n{c['n']}{c.get('act', 'bf16')}")
+def test_many_columns(vqv, case):
+    """Against the oracle; fewer ranks than the arrays hold, with NaN past them; in place, and columns of
+    wider tensors, whose rows are not 16-byte aligned and whose other columns stay."""
+    assert is_wide(case)
+    c = Case(**case)
+    x, which, N = c.x.cuda(), c.which.cuda(), case["N"]
+    want, ad = c.want(), c.set(vqv)
+    got = vqv.vqv_lora_add(x, ad, which, c.y.cuda())
+    c.close(got, want)
+    none = [m for m, e in enumerate(case["which"]) if not 0 <= e < case["n"]]
+    assert torch.equal(got.cpu()[none], c.y[none])
+    y = c.y.cuda()
+    vqv.vqv_lora_add(x, ad, which, y, out=y)
+    assert torch.equal(y, got)
+    for off, width in ((3, N + 6), (4, N + 12 - N % 4)):
+        wide = torch.full((len(which), width), 5.0, device="cuda")
+        wide[:, off:off + N] = c.y.cuda()
+        vqv.vqv_lora_add(x, ad, which, wide[:, off:off + N], out=wide[:, off:off + N])
+        assert torch.equal(wide[:, off:off + N], got)
+        assert (wide[:, :off] == 5).all() and (wide[:, off + N:] == 5).all()
+    c.ranks = torch.tensor([(5 * e + 3) % (case["rank"] + 1) for e in range(case["n"])], dtype=torch.int32)
+    for e, r in enumerate(c.ranks.tolist()):
+        c.a[e, r:] = float("nan")
+        c.b[e, :, r:] = float("nan")
+    c.close(vqv.vqv_lora_add(x, c.set(vqv), which, c.y.cuda()), c.want())

@@ -253,3 +253,25 @@ def test_refuses_wrong_tensors(vqv):
             vqv.vqv_verify_sampled(lg, d, u, 2, 3, **kw)
     with pytest.raises(vqv.VqvError):
         vqv.vqv_verify_sampled(lg, d, u, 2, 3, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("T,probs,uniform", [(1, False, 0.3), (2, True, 0.0), (2, True, 0.99), (2, False, 0.99)])
+def test_more_chunks_than_threads(vqv, T, probs, uniform):
+    """A vocabulary of more chunks (of 4096) than a draw has threads: a thread then has several."""
+    N = 1024 * 4096 + 9001
+    c = Case(B=1, T=T, N=N, probs=probs, seed=5, spread=1.0, near=0.2) if T == 1 else Case.__new__(Case)
+    if T > 1:   # torch.multinomial has its limit at 2^24 categories; the draft is any token
+        gen = torch.Generator().manual_seed(6)
+        c.B, c.T, c.N, c.temperature, c.lens = 1, T, N, torch.tensor([0.8]), None
+        c.logits = torch.randn(T, N, generator=gen)
+        c.probs = torch.softmax(c.logits[:1] / 0.8 + 0.2 * torch.randn(1, N, generator=gen), 1)[None] if probs else None
+        c.draft = torch.tensor([[N - 5]], dtype=torch.int32)
+        c.uniform = torch.tensor([[uniform, 0.6180339]])
+    else:
+        c.uniform[:] = uniform
+    tokens, accepts, logp, near = c.want()
+    token, accept, got = c.run(vqv)
+    assert accept.tolist() == accepts
+    # borders are 2^-22 of the sum apart, 64-bit sums of 2^22 terms off by far less than one
+    assert token.tolist() == tokens
+    assert ((got.cpu().double() - logp).abs() <= 2.0 ** -24 * logp.abs() + 2.0 ** -36).all()
