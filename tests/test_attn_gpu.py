@@ -453,3 +453,11 @@ def test_infinity_behind_a_small_weight(vqv, rows, dim, dtype):
             got = c.run(vqv, scale=0.6931471805599453)
             assert (got[:, :, 11] == x).all(), depth
             assert got.isfinite().sum() == got.numel() - got[:, :, 11].numel()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows,most", [(3, 64), (3, 4000), (50, 64), (300, 64)])
+def test_largest_scale(vqv, rows, most, dtype):
+    """A scale that log2(e) takes past fp32's range: one token takes all."""
+    c = Case(rows=[rows], kv=[400], heads=4, hk=2, dim=64, ps=16, dtype=dtype, seed=9, max_kv=most)
+    assert torch.equal(c.run(vqv, scale=3.4e38), c.want(scale=3.4e38)[0].to(c.t))

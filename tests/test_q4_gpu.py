@@ -667,3 +667,19 @@ def test_copied_workspace(vqv):
                               workspace=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
     h = planned(rows=[300], kv=[500], heads=4, hk=2, dim=128, ps=16, dtype="fp16")
     h.close(h.run(vqv), h.want())
+
+
+@pytest.mark.parametrize("rows,most", [(3, 64), (3, 4000), (50, 64), (300, 2 ** 18)])
+@pytest.mark.parametrize("size,scale", [(1e-38, 1e-6), (1e-30, 1e-30), (1e30, 1e30), (1.0, 3.4e38), (1.0, 1e-45)])
+def test_scales_of_any_size(vqv, rows, most, size, scale):
+    """All weights of a row the same, or one token that takes all: for rows of several tiles, splits and the copy."""
+    c = Case(rows=[rows], kv=[500], heads=4, hk=2, dim=64, ps=16, seed=9, max_kv=most)
+    c.q = (c.q.float() * size).to(c.t)
+    if size * scale > 1:
+        c.q = c.q.abs() + size            # the largest sum of keys takes all
+        k = torch.randn(500, 2, 1).expand(500, 2, 64) * torch.arange(500)[:, None, None] / 500
+        c.set(0, 0, k.contiguous())
+        c.q[:] = c.q[:, :, :1]
+    got, want = c.run(vqv, scale=scale), c.want(scale=scale)
+    c.close(got, want)
+    assert size * scale <= 1 or torch.equal(got, want[0].to(c.t))

@@ -136,7 +136,7 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
 #pragma unroll
     for (int s = 0; s < DS; ++s) qf[s] = scaled_to_half(qf[s], shift_q);
   }
-  const float scale_log2 = SAME ? a.scale_log2 : ldexpf(a.scale_log2, -shift_q);
+  const float scale_log2 = SAME ? a.scale_log2 : scale_of_row(a.scale_log2, shift_q);
 
   f32x16 o[DB];
 #pragma unroll

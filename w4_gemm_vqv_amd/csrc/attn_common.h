@@ -137,6 +137,13 @@ __device__ __forceinline__ s16x8 scaled_to_half(s16x8 v, int e) {
   return __builtin_bit_cast(s16x8, r);
 }
 
+// The scale of the scores of a row that is 2^e times itself, within fp32's normal range: as 0 or an
+// infinity it would turn a hidden score or a difference of 0 into NaN. At the bounds it stands for, all
+// weights of a row are the same or all but the largest 0, as of the true scale.
+__device__ __forceinline__ float scale_of_row(float scale_log2, int e) {
+  return fminf(fmaxf(ldexpf(scale_log2, -e), 0x1p-126f), 0x1p127f);
+}
+
 // Not 0 where one of two packed values is an infinity or NaN: an exponent of
 // ones carries into the sign's place.
 template <typename T>
@@ -481,7 +488,7 @@ inline AttnArgs attn_args(const void* q, void* out, const vqv_seqs& seqs, int pa
   }
   a.kv_heads = kv_heads;
   a.group = heads / kv_heads;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  a.scale_log2 = fminf(scale * 1.4426950408889634f, 0x1p127f);
   a.window = window;
   a.sinks = window > 0 ? sinks : 0;
   a.groups = plan.groups;

@@ -350,7 +350,7 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
 #pragma unroll
       for (int x = 0; x < KS; ++x) qf[r][x] = scaled_to_half(qf[r][x], shift_q[r]);
     }
-    scale[r] = ldexpf(a.scale_log2, -shift_q[r]);
+    scale[r] = scale_of_row(a.scale_log2, shift_q[r]);
   }
 
   f32x4 o[RT][DT];
