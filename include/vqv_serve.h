@@ -95,10 +95,17 @@ vqv_status vqv_cache_q4_read(const vqv_cache_q4* cache, int layer, const vqv_seq
  * (to 2^-22) where max_rows rows of a key head's queries are 64 or fewer.
  * Weights 2^29 below the largest are off by up to 2^-39 of it.
  * The workspace of large bf16 calls without a window (prompt chunks) holds the
- * tokens of their sequences in fp16, 1 GiB at most; fp16 calls use less of it.
+ * tokens of their sequences in fp16, beside what other calls need. Where they
+ * would take more than 1 GiB they have 1 GiB, and the sequences that do not fit it
+ * are read as in smaller calls: this share does not fall as a call grows.
+ * vqv_paged_attn_q4_workspace_bytes is enough for either type, ..type_workspace_bytes
+ * for queries of `dtype` (fp16 calls hold no such tokens). A call refuses a
+ * workspace that is smaller than its own type's.
  */
 size_t vqv_paged_attn_q4_workspace_bytes(const vqv_cache_q4* cache, const vqv_seqs* seqs,
                                          int heads, int window, int sinks);
+size_t vqv_paged_attn_q4_type_workspace_bytes(const vqv_cache_q4* cache, const vqv_seqs* seqs,
+                                              vqv_dtype dtype, int heads, int window, int sinks);
 
 vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4* cache, int layer,
                              const vqv_seqs* seqs, int heads, float scale, int window, int sinks,

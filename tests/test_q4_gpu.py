@@ -683,3 +683,45 @@ def test_scales_of_any_size(vqv, rows, most, size, scale):
     got, want = c.run(vqv, scale=scale), c.want(scale=scale)
     c.close(got, want)
     assert size * scale <= 1 or torch.equal(got, want[0].to(c.t))
+
+
+@pytest.mark.parametrize("case", [
+    dict(rows=[300, 260, 280], kv=[300, 700, 900], heads=4),             # 512 pairs and more each: the first fit
+    dict(rows=[4, 300, 1, 3, 270, 2, 290], kv=[90, 300, 33, 80, 700, 9, 500], heads=4),
+    dict(rows=[140, 1, 300], kv=[200, 40, 420], heads=8)])
+@pytest.mark.parametrize("width", [2 ** 20, 45000])
+def test_copies_that_do_not_fit(vqv, case, width):
+    """Tables of so many pages that the copy holds one or two of the sequences: the others are read
+    from the records, in the same call."""
+    c = planned(**case, hk=2, dim=64, ps=16)
+    c.max_kv = 16 * width
+    c.table = [row + [-1] * (width - len(row)) for row in c.table]
+    want = c.want()
+    c.close(c.run(vqv), want)
+    need = vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads)
+    assert 2 ** 30 <= need < 2 ** 30 + 2 ** 28
+    c.table[-1] = [-1] * width
+    got = c.run(vqv)
+    assert (got[c.start[-2]:] == 0).all()
+    c.close(got, c.want())
+
+
+def test_workspace_of_fp16_calls(vqv):
+    """fp16 calls need less than bf16 ones where those copy, and no less than they say."""
+    for rows, kv, most in ([300, 9], [500, 1400], 2 ** 17), ([8], [3000], 3000):
+        c = Case(rows=rows, kv=kv, heads=4, hk=2, dim=128, ps=16, dtype="fp16", max_kv=most)
+        want = c.run(vqv)
+        c.close(want, c.want())
+        need = vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads, dtype=torch.float16)
+        both = vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads)
+        assert need == both if max(rows) < 256 else need < both
+        assert vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads, dtype=torch.bfloat16) == both
+        with pytest.raises(ValueError):
+            vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads, dtype=torch.float32)
+        out = torch.empty(c.q.shape, dtype=c.t, device="cuda")
+        ws = torch.full((need + 16,), 255, dtype=torch.uint8, device="cuda")
+        vqv.vqv_paged_attn_q4(c.qd, c.cache, c.seqs, scale=c.scale, out=out, workspace=ws[:need])
+        assert torch.equal(out.cpu(), want) and (ws[need:] == 255).all()
+        if need:
+            with pytest.raises(vqv.VqvError, match="(?i)workspace"):
+                vqv.vqv_paged_attn_q4(c.qd, c.cache, c.seqs, scale=c.scale, out=out, workspace=ws[:need - 16])

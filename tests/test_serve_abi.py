@@ -259,3 +259,35 @@ def test_lora_columns_past_32_bits(S, L, N):
     assert lora_call(S, L, ad, M=1, ys=N, os=N, wn=1 << 60) == UNSUP
     assert L.vqv_lora_add_workspace_bytes(ad, 1) == 0
     assert L.vqv_lora_add_workspace_bytes(adapters(S, n=1, rank=8, K=8, N=2 ** 31 - 4097), 1) > 0
+
+
+def attn_bytes(S, L, dtype=None, heads=32, **kw):
+    width = -(-kw["max_kv"] // 64) + 1
+    c = cache(S, page_size=64, page_stride=64 * 8 * 80, layers=1)
+    s = seqs(S, table_width=width, table_stride=width, **kw)
+    if dtype is None:
+        return L.vqv_paged_attn_q4_workspace_bytes(c, s, heads, 0, 0)
+    return L.vqv_paged_attn_q4_type_workspace_bytes(c, s, dtype, heads, 0, 0)
+
+
+def test_copy_of_large_calls(S, L):
+    """The size of a prompt chunk's workspace does not collapse where its tokens take more than 1 GiB."""
+    for rows in (256, 1024, 2048):
+        for n in (1, 3):
+            got = [attn_bytes(S, L, n_seqs=n, n_rows=n * rows, max_rows=rows, max_kv=1 << i) for i in range(9, 24)]
+            got += [attn_bytes(S, L, n_seqs=n, n_rows=n * rows, max_rows=rows, max_kv=kv)
+                    for kv in (1 << 24, 20000011, 1 << 25)]
+            assert got[-1] >= 1 << 30 and all(b >= 0.9 * a for a, b in zip(got, got[1:])), got
+    got = [attn_bytes(S, L, n_seqs=n, n_rows=n * 1024, max_rows=1024, max_kv=32768) for n in range(1, 40)]
+    assert got[0] > 1 << 27 and got[-1] >= 1 << 30 and all(b >= 0.9 * a for a, b in zip(got, got[1:])), got
+
+
+def test_workspace_of_a_type(S, L):
+    """bf16 calls need what either type may; fp16 ones hold no copy."""
+    kw = dict(n_seqs=1, n_rows=2048, max_rows=2048, max_kv=10240)
+    assert attn_bytes(S, L, BF16, **kw) == attn_bytes(S, L, **kw) > 10240 * 8 * 128 * 4
+    assert attn_bytes(S, L, FP16, **kw) <= attn_bytes(S, L, **kw) - 10240 * 8 * 128 * 4
+    kw = dict(n_seqs=4, n_rows=32, max_rows=8, max_kv=8000)
+    assert attn_bytes(S, L, FP16, **kw) == attn_bytes(S, L, BF16, **kw) == attn_bytes(S, L, **kw) > 0
+    assert attn_bytes(S, L, FP32, **kw) == attn_bytes(S, L, 7, **kw) == 0
+    assert attn_bytes(S, L, FP16, heads=33, **kw) == 0

@@ -584,11 +584,11 @@ hipError_t launch_paged_attn(const void* q, const vqv_cache& c, int layer, const
 }
 
 hipError_t launch_paged_attn_copied(const void* q, const vqv_cache& c, const vqv_seqs& seqs,
-                                    int heads, float scale, int copied_len, void* out,
+                                    int heads, float scale, const Copied& copied, void* out,
                                     void* workspace, const AttnPlan& plan, hipStream_t stream) {
   AttnArgs a = args_of(q, c, 0, seqs, heads, scale, 0, 0, out, workspace, plan);
   a.which = kCopied;
-  a.copied_len = copied_len;
+  a.copied = copied;
   return launch_copied(a, c.dim, stream);
 }
 

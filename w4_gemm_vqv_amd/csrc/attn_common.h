@@ -43,7 +43,8 @@ struct AttnArgs {
   float scale_log2;
   int window, sinks;
   int groups, split_blocks, splits;  // work-groups over a sequence's rows; of its tokens
-  int which, copied_len;             // of kAll, kCopied, kOthers; tokens that a copy holds
+  int which;                         // of kAll, kCopied, kOthers
+  Copied copied;
   float* part;  // [n_rows * heads][splits][dim] sums, then [..][splits][2] (max, sum)
   float* part_ml;
 };
@@ -376,13 +377,15 @@ __device__ __forceinline__ int tokens_of(const AttnArgs& a, int kv_len) {
   return (int)min((int64_t)kv_len, min(room, (int64_t)1 << 30));
 }
 
-__device__ __forceinline__ bool is_copied(const vqv_seqs& s, int b, int group, int copied_len) {
-  const int n = min(min(s.row_start[b + 1], s.n_rows) - max(s.row_start[b], 0), s.max_rows);
-  return n * group >= kCopiedPairs && s.kv_len[b] <= copied_len;
+__device__ __forceinline__ bool is_copied(const vqv_seqs& s, int b, int group, const Copied& c) {
+  const int row0 = max(s.row_start[b], 0);
+  const int n = min(min(s.row_start[b + 1], s.n_rows) - row0, s.max_rows);
+  return n * group >= kCopiedPairs && s.kv_len[b] <= c.len &&
+         (c.by_number ? b : row0 * group / kCopiedPairs) < c.slots;
 }
 
 __device__ __forceinline__ bool not_of_this_call(const AttnArgs& a, int b) {
-  return a.which != kAll && is_copied(a.seqs, b, a.group, a.copied_len) != (a.which == kCopied);
+  return a.which != kAll && is_copied(a.seqs, b, a.group, a.copied) != (a.which == kCopied);
 }
 
 // Blocks of a split: the plan's, or more where a sequence is longer than the
@@ -495,7 +498,6 @@ inline AttnArgs attn_args(const void* q, void* out, const vqv_seqs& seqs, int pa
   a.split_blocks = plan.split_blocks;
   a.splits = plan.splits;
   a.which = kAll;
-  a.copied_len = 0;
   a.part = static_cast<float*>(workspace);
   a.part_ml = a.part + (size_t)seqs.n_rows * heads * plan.splits * dim;
   return a;

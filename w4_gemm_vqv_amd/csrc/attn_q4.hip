@@ -770,7 +770,7 @@ size_t attn_q4_partial_bytes(const vqv_cache_q4& c, const vqv_seqs& s, int heads
 
 hipError_t launch_paged_attn_q4(const void* q, int dtype, const vqv_cache_q4& c, int layer,
                                 const vqv_seqs& seqs, int heads, float scale, int window,
-                                int sinks, int copied_len, void* out, void* workspace,
+                                int sinks, const Copied& copied, void* out, void* workspace,
                                 const AttnPlan& plan, hipStream_t stream) {
   AttnArgs a = attn_args(q, out, seqs, c.page_size, c.pages, c.kv_heads, heads, c.dim, scale,
                          window, sinks, workspace, plan);
@@ -779,8 +779,8 @@ hipError_t launch_paged_attn_q4(const void* q, int dtype, const vqv_cache_q4& c,
   a.page_units = (unsigned)(c.page_stride >> 4);
   a.slot_units = (unsigned)(c.slot_stride >> 4);
   a.head_units = (unsigned)(c.head_stride >> 4);
-  if (copied_len > 0) a.which = kOthers;
-  a.copied_len = copied_len;
+  if (copied.slots > 0) a.which = kOthers;
+  a.copied = copied;
   const bool few = pairs_of(seqs, heads, c.kv_heads) <= 64;
   return dtype == VQV_BF16 ? launch_type<__bf16>(a, c.dim, plan, few, stream)
                            : launch_type<_Float16>(a, c.dim, plan, few, stream);

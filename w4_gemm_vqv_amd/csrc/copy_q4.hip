@@ -12,7 +12,10 @@
 //
 // A sequence's place in the copy is its number or, where rows leave fewer that can
 // be copied, floor(first pair / kCopiedPairs): those that are copied have
-// kCopiedPairs or more each, so no two get the same one.
+// kCopiedPairs or more each, so no two get the same one. Where not all of them fit
+// kMostBytes, the copy has that size, whatever else the call grows by: it holds the
+// sequences of the first places that do, each up to as many pages as fit alone, and
+// the others are read from the records.
 
 #include "attn_common.h"
 #include "round_common.h"
@@ -22,7 +25,7 @@ namespace vqv {
 namespace {
 
 constexpr int kTokens = 16;              // of a work-group
-constexpr size_t kMostBytes = 1u << 30;  // of a copy; larger calls read the records
+constexpr size_t kMostBytes = 1u << 30;  // of a copy
 
 // Scores (rows * heads * tokens of the longest sequence) from which the copy pays
 // for itself and two more launches, with 32 heads of 128 on 8: at 2^27 114 us become
@@ -36,8 +39,8 @@ struct CopyArgs {
   int64_t page_stride, slot_stride, head_stride;
   int pages, page_size, kv_heads, group;
   vqv_seqs seqs;
-  int copied_len, width, chunks;
-  bool by_number;  // a sequence's place is its number
+  Copied copied;
+  int width, chunks;
   uint16_t* kc;
   uint16_t* vc;
   int32_t* table;
@@ -55,14 +58,14 @@ __global__ __launch_bounds__(threads(D)) void copy_q4(const CopyArgs a) {
   const int part = blockIdx.x / a.kv_heads, h = blockIdx.x % a.kv_heads;
   const int slot = part / a.chunks;
   int b = slot;
-  if (!a.by_number) {
+  if (!a.copied.by_number) {
     // A copied sequence whose first pair is in the slot's range has the range's
     // last row too.
     const int row = ((slot + 1) * kCopiedPairs + a.group - 1) / a.group - 1;
     b = seq_of_row(a.seqs.row_start, a.seqs.n_seqs, row);
     if (b >= a.seqs.n_seqs || max(a.seqs.row_start[b], 0) * a.group / kCopiedPairs != slot) return;
   }
-  if (!is_copied(a.seqs, b, a.group, a.copied_len)) return;
+  if (!is_copied(a.seqs, b, a.group, a.copied)) return;
 
   const int t = part % a.chunks * kTokens + threadIdx.x / PER, piece = threadIdx.x % PER;
   const int i = t / a.page_size, s = t % a.page_size;
@@ -107,16 +110,26 @@ CopyPlan copy_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int wind
   if (window > 0 || (int64_t)rows * group < kCopiedPairs) return p;
   if ((double)rows * heads * s.max_kv < kLeastScores || s.table_width < 1) return p;
   const int64_t most = (int64_t)s.n_rows * group / kCopiedPairs;
-  const int64_t slots = most < s.n_seqs ? most : s.n_seqs;
+  int64_t slots = most < s.n_seqs ? most : s.n_seqs;
+  p.copied.by_number = slots == s.n_seqs;
   int64_t width = ((int64_t)s.max_kv + c.page_size - 1) / c.page_size;
   if (width > s.table_width) width = s.table_width;
-  const double values = (double)slots * width * c.page_size * c.kv_heads * c.dim * 2;
-  const double table = (double)s.n_seqs * width * 4;
-  if (2 * values + table > (double)kMostBytes) return p;
+  // Of a page's keys (values), and of an entry of each sequence's table.
+  const double page = (double)c.page_size * c.kv_heads * c.dim * 2, entries = 4.0 * s.n_seqs;
+  const bool all = (2 * slots * page + entries) * width + 16 <= (double)kMostBytes;
+  if (!all) {
+    const int64_t fit = (int64_t)((kMostBytes - 16) / (2 * page + entries));
+    if (fit < 1) return p;
+    if (width > fit) width = fit;
+    const int64_t held = (int64_t)((kMostBytes - 16 - entries * width) / (2 * page * width));
+    if (slots > held) slots = held;
+  }
+  const int64_t tokens = width * c.page_size;
+  p.copied.len = tokens < s.max_kv && width < s.table_width ? (int)tokens : s.max_kv;
+  p.copied.slots = (int)slots;
   p.width = (int)width;
-  p.slots = (int)slots;
-  p.values = (size_t)values;
-  p.table = ((size_t)table + 15) / 16 * 16;
+  p.values = (size_t)(slots * width) * (size_t)page;
+  p.bytes = all ? (2 * p.values + (size_t)(entries * width) + 15) / 16 * 16 : kMostBytes;
   p.attn = attn_plan(copy_cache(c, p, nullptr), copy_seqs(s, p, nullptr), heads, 0, 0);
   if ((int64_t)c.kv_heads * s.n_seqs * p.attn.groups * p.attn.splits >= (1ll << 23) ||
       (p.attn.splits > 1 && (int64_t)s.n_rows * heads >= (1ll << 24)))
@@ -130,7 +143,7 @@ vqv_cache copy_cache(const vqv_cache_q4& c, const CopyPlan& p, void* workspace) 
   r.v = static_cast<char*>(workspace) + p.values;
   r.dtype = VQV_FP16;
   r.layers = 1;
-  r.pages = p.slots * p.width;
+  r.pages = p.copied.slots * p.width;
   r.page_size = c.page_size;
   r.kv_heads = c.kv_heads;
   r.dim = c.dim;
@@ -162,20 +175,19 @@ hipError_t launch_copy_q4(const vqv_cache_q4& c, int layer, const vqv_seqs& s, i
                    c.kv_heads,
                    heads / c.kv_heads,
                    s,
-                   s.max_kv,
+                   p.copied,
                    p.width,
-                   ceil_div(tokens < s.max_kv ? tokens : s.max_kv, kTokens),
-                   p.slots == s.n_seqs,
+                   ceil_div(tokens < p.copied.len ? tokens : p.copied.len, kTokens),
                    static_cast<uint16_t*>(workspace),
                    reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + p.values),
                    reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + 2 * p.values)};
   switch (c.dim) {
-    case 64: return launch_dim<64>(a, p.slots, stream);
-    case 80: return launch_dim<80>(a, p.slots, stream);
-    case 96: return launch_dim<96>(a, p.slots, stream);
-    case 128: return launch_dim<128>(a, p.slots, stream);
-    case 192: return launch_dim<192>(a, p.slots, stream);
-    default: return launch_dim<256>(a, p.slots, stream);
+    case 64: return launch_dim<64>(a, p.copied.slots, stream);
+    case 80: return launch_dim<80>(a, p.copied.slots, stream);
+    case 96: return launch_dim<96>(a, p.copied.slots, stream);
+    case 128: return launch_dim<128>(a, p.copied.slots, stream);
+    case 192: return launch_dim<192>(a, p.copied.slots, stream);
+    default: return launch_dim<256>(a, p.copied.slots, stream);
   }
 }
 

@@ -39,10 +39,17 @@ hipError_t launch_paged_attn(const void* q, const vqv_cache& cache, int layer,
                              void* out, void* workspace, const AttnPlan& plan,
                              hipStream_t stream);
 
+// Which sequences of a 4-bit cache are read through a 16-bit copy: those of many rows and up to
+// `len` tokens whose place in the copy is below `slots` (0: none). A place is the sequence's
+// number or goes by its first row.
+struct Copied {
+  int len, slots;
+  bool by_number;
+};
 // bf16 queries and outputs over an fp16 cache, of the sequences that are copied to
 // it, without a window; plans of 512 (row, head) pairs or more.
 hipError_t launch_paged_attn_copied(const void* q, const vqv_cache& cache, const vqv_seqs& seqs,
-                                    int heads, float scale, int copied_len, void* out,
+                                    int heads, float scale, const Copied& copied, void* out,
                                     void* workspace, const AttnPlan& plan, hipStream_t stream);
 
 hipError_t launch_cache_copy(const vqv_cache& cache, const int32_t* src, const int32_t* dst,

@@ -117,7 +117,7 @@ namespace {
 
 // What vqv_paged_attn_q4 checks of its sizes, and the plan.
 vqv_status plan_attn_q4(const vqv_cache_q4* cache, const vqv_seqs* seqs, int heads, int window,
-                        int sinks, vqv::AttnPlan* plan, vqv::CopyPlan* copy) {
+                        int sinks, vqv_dtype dtype, vqv::AttnPlan* plan, vqv::CopyPlan* copy) {
   vqv_status st = check_cache_q4(cache);
   if (st != VQV_OK) return st;
   if ((st = check_seqs(seqs)) != VQV_OK) return st;
@@ -130,7 +130,8 @@ vqv_status plan_attn_q4(const vqv_cache_q4* cache, const vqv_seqs* seqs, int hea
   if ((int64_t)cache->kv_heads * seqs->n_seqs * plan->groups * plan->splits >= (1ll << 23))
     return VQV_ERR_UNSUPPORTED;  // threads of a grid are counted in 32 bits
   if (plan->splits > 1 && (int64_t)seqs->n_rows * heads >= (1ll << 24)) return VQV_ERR_UNSUPPORTED;
-  *copy = vqv::copy_plan(*cache, *seqs, heads, window);
+  // fp16 keys as one value each would be the larger part of fp16 outputs' error.
+  *copy = dtype == VQV_BF16 ? vqv::copy_plan(*cache, *seqs, heads, window) : vqv::CopyPlan{};
   return VQV_OK;
 }
 
@@ -139,11 +140,11 @@ vqv_status plan_attn_q4(const vqv_cache_q4* cache, const vqv_seqs* seqs, int hea
 size_t attn_q4_bytes(const vqv_cache_q4& cache, const vqv_seqs& seqs, int heads,
                      const vqv::AttnPlan& plan, const vqv::CopyPlan& copy) {
   size_t part = vqv::attn_q4_partial_bytes(cache, seqs, heads, plan);
-  if (copy.slots == 0) return part;
+  if (copy.copied.slots == 0) return part;
   const size_t wide =
       vqv::attn_partial_bytes(vqv::copy_cache(cache, copy, nullptr), seqs, heads, copy.attn);
   if (wide > part) part = wide;
-  return (part + 15) / 16 * 16 + copy.bytes();
+  return (part + 15) / 16 * 16 + copy.bytes;
 }
 
 }  // namespace
@@ -154,7 +155,17 @@ size_t vqv_paged_attn_q4_workspace_bytes(const vqv_cache_q4* cache, const vqv_se
                                          int heads, int window, int sinks) {
   vqv::AttnPlan plan;
   vqv::CopyPlan copy;
-  if (plan_attn_q4(cache, seqs, heads, window, sinks, &plan, &copy) != VQV_OK) return 0;
+  if (plan_attn_q4(cache, seqs, heads, window, sinks, VQV_BF16, &plan, &copy) != VQV_OK) return 0;
+  return attn_q4_bytes(*cache, *seqs, heads, plan, copy);
+}
+
+size_t vqv_paged_attn_q4_type_workspace_bytes(const vqv_cache_q4* cache, const vqv_seqs* seqs,
+                                              vqv_dtype dtype, int heads, int window, int sinks) {
+  vqv::AttnPlan plan;
+  vqv::CopyPlan copy;
+  if (!half_type(dtype) ||
+      plan_attn_q4(cache, seqs, heads, window, sinks, dtype, &plan, &copy) != VQV_OK)
+    return 0;
   return attn_q4_bytes(*cache, *seqs, heads, plan, copy);
 }
 
@@ -164,7 +175,7 @@ vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4*
                              void* hip_stream) {
   vqv::AttnPlan plan;
   vqv::CopyPlan copy;
-  const vqv_status st = plan_attn_q4(cache, seqs, heads, window, sinks, &plan, &copy);
+  const vqv_status st = plan_attn_q4(cache, seqs, heads, window, sinks, dtype, &plan, &copy);
   if (st != VQV_OK) return st;
   if ((seqs->n_rows && (!q || !out)) || layer < 0 || layer >= cache->layers) return VQV_ERR_ARG;
   if (dtype == VQV_FP32) return VQV_ERR_UNSUPPORTED;
@@ -172,8 +183,6 @@ vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4*
   if (!(scale > 0.0f) || !isfinite(scale)) return VQV_ERR_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return VQV_ERR_ALIGN;
   const size_t bytes = (size_t)seqs->n_rows * heads * cache->dim * 2;
-  // fp16 keys as one value each would be the larger part of fp16 outputs' error.
-  if (dtype != VQV_BF16) copy = {};
   const size_t need = attn_q4_bytes(*cache, *seqs, heads, plan, copy);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return VQV_ERR_WORKSPACE;
@@ -183,18 +192,18 @@ vqv_status vqv_paged_attn_q4(const void* q, vqv_dtype dtype, const vqv_cache_q4*
   if (seqs->n_rows == 0 || seqs->max_rows == 0) return VQV_OK;
   (void)hipGetLastError();
   const auto stream = static_cast<hipStream_t>(hip_stream);
-  if (copy.slots) {
-    void* held = static_cast<char*>(workspace) + (need - copy.bytes());
+  if (copy.copied.slots) {
+    void* held = static_cast<char*>(workspace) + (need - copy.bytes);
     hipError_t e = vqv::launch_copy_q4(*cache, layer, *seqs, heads, copy, held, stream);
     if (e == hipSuccess)
       e = vqv::launch_paged_attn_copied(q, vqv::copy_cache(*cache, copy, held),
                                         vqv::copy_seqs(*seqs, copy, held), heads, scale,
-                                        seqs->max_kv, out, workspace, copy.attn, stream);
+                                        copy.copied, out, workspace, copy.attn, stream);
     if (e != hipSuccess) return status_of(e);
   }
   return status_of(vqv::launch_paged_attn_q4(q, (int)dtype, *cache, layer, *seqs, heads, scale,
-                                             window, sinks, copy.slots ? seqs->max_kv : 0, out,
-                                             workspace, plan, stream));
+                                             window, sinks, copy.copied, out, workspace, plan,
+                                             stream));
 }
 
 }  // extern "C"

@@ -18,23 +18,23 @@ hipError_t launch_rope_append_q4(const RowsIn& q, const RowsIn& k, const RowsIn&
 hipError_t launch_cache_q4_read(const vqv_cache_q4& cache, int layer, const vqv_seqs& seqs,
                                 void* k_out, void* v_out, int out_dtype, hipStream_t stream);
 
-// copied_len: sequences of many rows and up to that many tokens are left out (0: none).
 AttnPlan attn_q4_plan(const vqv_cache_q4& cache, const vqv_seqs& seqs, int heads, int window,
                       int sinks);
 size_t attn_q4_partial_bytes(const vqv_cache_q4& cache, const vqv_seqs& seqs, int heads,
                              const AttnPlan& plan);
+// The sequences that are not `copied`.
 hipError_t launch_paged_attn_q4(const void* q, int dtype, const vqv_cache_q4& cache, int layer,
                                 const vqv_seqs& seqs, int heads, float scale, int window,
-                                int sinks, int copied_len, void* out, void* workspace,
+                                int sinks, const Copied& copied, void* out, void* workspace,
                                 const AttnPlan& plan, hipStream_t stream);
 
 // The tokens of sequences of many rows as fp16, in the workspace.
 struct CopyPlan {
-  int slots;  // sequences that it holds, 0: nothing is copied
-  int width;  // pages of each
-  size_t values, table;  // bytes of keys (values), of the pages' table
+  Copied copied;  // slots 0: nothing is
+  int width;      // pages of a sequence
+  size_t values;  // bytes of keys (values); the pages' table is behind them
+  size_t bytes;   // in all
   AttnPlan attn;
-  size_t bytes() const { return slots ? 2 * values + table : 0; }
 };
 CopyPlan copy_plan(const vqv_cache_q4& cache, const vqv_seqs& seqs, int heads, int window);
 vqv_cache copy_cache(const vqv_cache_q4& cache, const CopyPlan& plan, void* workspace);

@@ -20,8 +20,8 @@ from .vqv import _on_device
 from .vqv import lib as _load
 
 SERVE_EXPORTS = ("vqv_q4_record_bytes", "vqv_rope_append_q4", "vqv_cache_q4_read",
-                 "vqv_paged_attn_q4_workspace_bytes", "vqv_paged_attn_q4",
-                 "vqv_verify_sampled_workspace_bytes", "vqv_verify_sampled",
+                 "vqv_paged_attn_q4_workspace_bytes", "vqv_paged_attn_q4_type_workspace_bytes",
+                 "vqv_paged_attn_q4", "vqv_verify_sampled_workspace_bytes", "vqv_verify_sampled",
                  "vqv_lora_add_workspace_bytes", "vqv_lora_add")
 
 _vp, _i, _i64, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -54,6 +54,7 @@ def _serve_lib() -> ctypes.CDLL:
                                             _i, cache, _i, seqs, rope, _vp, _i, _vp]),
                 ("vqv_cache_q4_read", _i, [cache, _i, seqs, _vp, _vp, _i, _vp]),
                 ("vqv_paged_attn_q4_workspace_bytes", _sz, [cache, seqs, _i, _i, _i]),
+                ("vqv_paged_attn_q4_type_workspace_bytes", _sz, [cache, seqs, _i, _i, _i, _i]),
                 ("vqv_paged_attn_q4", _i, [_vp, _i, cache, _i, seqs, _i, f32, _i, _i, _vp, _vp,
                                            _sz, _vp]),
                 ("vqv_verify_sampled_workspace_bytes", _sz, [_i, _i, _i]),
@@ -161,7 +162,14 @@ def vqv_cache_q4_read(cache: PagedCacheQ4, seqs: Sequences, layer: int = 0,
 
 
 def vqv_paged_attn_q4_workspace_bytes(cache: PagedCacheQ4, seqs: Sequences, heads: int,
-                                      window: int = 0, sinks: int = 0) -> int:
+                                      window: int = 0, sinks: int = 0,
+                                      dtype: torch.dtype | None = None) -> int:
+    """Bytes that a call needs, of queries of `dtype` or (None) of either type."""
+    if dtype is not None:
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"queries are bf16 or fp16, not {dtype}")
+        return _serve_lib().vqv_paged_attn_q4_type_workspace_bytes(
+            cache.c, seqs.c, _DTYPES[dtype], heads, window, sinks)
     return _serve_lib().vqv_paged_attn_q4_workspace_bytes(cache.c, seqs.c, heads, window, sinks)
 
 
@@ -181,8 +189,8 @@ def vqv_paged_attn_q4(q: torch.Tensor, cache: PagedCacheQ4, seqs: Sequences, sca
     if out is None:
         out = _new(shape, q.dtype, dev, stream)
     op = _take(out, "out", shape, q.dtype, dev)
-    need = 0 if workspace is not None else vqv_paged_attn_q4_workspace_bytes(cache, seqs, heads,
-                                                                             window, sinks)
+    need = 0 if workspace is not None else vqv_paged_attn_q4_workspace_bytes(
+        cache, seqs, heads, window, sinks, q.dtype)
     workspace, wp, wn = _scratch(workspace, need, dev, stream)
     _check(_on_device(
         dev, _serve_lib().vqv_paged_attn_q4, qp, _DTYPES[q.dtype], cache.c, layer, seqs.c, heads,
