@@ -461,3 +461,15 @@ def test_largest_scale(vqv, rows, most, dtype):
     """A scale that log2(e) takes past fp32's range: one token takes all."""
     c = Case(rows=[rows], kv=[400], heads=4, hk=2, dim=64, ps=16, dtype=dtype, seed=9, max_kv=most)
     assert torch.equal(c.run(vqv, scale=3.4e38), c.want(scale=3.4e38)[0].to(c.t))
+
+
+@pytest.mark.parametrize("n", [2, 3, 4, 8, 9])
+def test_chunk_beside_decoding_rows(vqv, n):
+    """Tiles of one long chunk and single rows, in batches of even and odd size, the chunk first and last."""
+    for first in (True, False):
+        rows = [150] + [1] * (n - 1)
+        kv = [400] + [(113 * i) % 500 + 1 for i in range(1, n)]
+        if not first:
+            rows, kv = rows[::-1], kv[::-1]
+        c = Case(rows=rows, kv=kv, heads=4, hk=2, dim=64, ps=16, seed=n)
+        c.close(c.run(vqv), c.want())

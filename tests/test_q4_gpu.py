@@ -725,3 +725,18 @@ def test_workspace_of_fp16_calls(vqv):
         if need:
             with pytest.raises(vqv.VqvError, match="(?i)workspace"):
                 vqv.vqv_paged_attn_q4(c.qd, c.cache, c.seqs, scale=c.scale, out=out, workspace=ws[:need - 16])
+
+
+@pytest.mark.parametrize("n", [2, 3, 4, 8, 9, 16])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_chunk_beside_decoding_rows(vqv, n, dtype):
+    """Tiles of one long chunk and single rows, in batches of even and odd size, the chunk first and last."""
+    for first in (True, False):
+        rows = [150] + [1] * (n - 1)
+        kv = [700] + [(113 * i) % 900 + 1 for i in range(1, n)]
+        if not first:
+            rows, kv = rows[::-1], kv[::-1]
+        c = Case(rows=rows, kv=kv, heads=4, hk=2, dim=64, ps=16, dtype=dtype, seed=n)
+        c.close(c.run(vqv), c.want())
+        c.max_kv = 9000     # planned for longer ones: splits
+        c.close(c.run(vqv), c.want())
