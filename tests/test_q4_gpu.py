@@ -727,6 +727,16 @@ def test_workspace_of_fp16_calls(vqv):
                 vqv.vqv_paged_attn_q4(c.qd, c.cache, c.seqs, scale=c.scale, out=out, workspace=ws[:need - 16])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_many_sequences(vqv, dtype):
+    """64 of very different lengths, that fill the GPU and are split all the same."""
+    kv = [9000, 1] + [(37 * i) % 300 + 1 for i in range(62)]
+    c = Case(rows=[1] * 64, kv=kv, heads=8, hk=8, dim=64, ps=16, dtype=dtype)
+    c.close(c.run(vqv), c.want(), low=5.0 * 9000)
+    assert vqv.vqv_paged_attn_q4_workspace_bytes(c.cache, c.seqs, c.heads) > 0
+    c.close(c.run(vqv, 300, 5), c.want(300, 5))
+
+
 @pytest.mark.parametrize("n", [2, 3, 4, 8, 9, 16])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_chunk_beside_decoding_rows(vqv, n, dtype):

@@ -291,3 +291,15 @@ def test_workspace_of_a_type(S, L):
     assert attn_bytes(S, L, FP16, **kw) == attn_bytes(S, L, BF16, **kw) == attn_bytes(S, L, **kw) > 0
     assert attn_bytes(S, L, FP32, **kw) == attn_bytes(S, L, 7, **kw) == 0
     assert attn_bytes(S, L, FP16, heads=33, **kw) == 0
+
+
+def test_long_sequences_are_split(S, L):
+    """Sequences of 16383 tokens are split over work-groups however many decode (partial sums need a
+    workspace), but a call is not refused for its splits."""
+    for n in (8, 48, 63, 64, 128, 200):
+        assert attn_bytes(S, L, n_seqs=n, n_rows=n, max_rows=1, max_kv=16383) > 0, n
+    assert attn_bytes(S, L, n_seqs=48, n_rows=256 + 47, max_rows=256, max_kv=16383) > 0
+    for n, heads in ((65535, 64), (40000, 128)):
+        s = seqs(S, n_seqs=n, n_rows=n, max_rows=1, max_kv=1 << 20, table_width=1 << 16, table_stride=1 << 16)
+        c = cache(S, kv_heads=8, page_size=16)
+        assert attn_call(S, L, c=c, s=s, heads=heads, ws=None, wn=0, q=None) == ARG   # refused for q, not for its size

@@ -747,18 +747,29 @@ AttnPlan attn_q4_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int w
     tokens = seen < tokens ? seen : tokens;
   }
   const int blocks = ceil_div(tokens < 1 ? 1 : tokens, bt);
-  const int64_t base = (int64_t)c.kv_heads * s.n_seqs * p.groups;
-  // Blocks of a split: all, where the rows alone fill the GPU; else as many as
-  // leave a work-group to each CU, and no more than 1024 tokens' worth unless
-  // that were more than 16 rounds of work-groups (48 ragged sequences: 164 us,
-  // with 2048 tokens 174, with 4096 201).
+  // Work-groups that have rows, of all sequences.
+  const int64_t grid = (int64_t)c.kv_heads * s.n_seqs * p.groups;
+  const int64_t tiles = (int64_t)s.n_rows * (heads / c.kv_heads) / (16 * p.mw) + s.n_seqs;
+  const int64_t base = c.kv_heads * tiles < grid ? c.kv_heads * tiles : grid;
+  // Blocks of a split: as many as leave a work-group to each CU, and no more than
+  // 1024 tokens' worth unless that were more than 16 rounds of work-groups (48
+  // ragged sequences: 164 us, with 2048 tokens 174, with 4096 201).
+  // Where the rows alone fill the GPU: all, unless few work-groups have long
+  // sequences, of which the longest would end alone (ragged to 16383 tokens, one
+  // row each, split and whole: 64 sequences 217 and 277 us, 128 453 and 550; 32 x 16
+  // rows to 32768 413 and 630). Else the join costs more than it gives (2.7 ns a row
+  // and head: 256 sequences of 4 rows to 4096 255 and 229 us, 128 of 8 rows to 8192
+  // 296 and 276, a chunk of 512 rows over 4096 138 and 93).
   const int most = 1024 / bt;
   int64_t per = ceil_div(blocks * base, 256);
-  if (base >= 512) {
+  const bool uneven = base < (p.mw == 1 ? 2048 : 1024) && s.n_seqs > 1 && blocks >= 8 * most;
+  if (base >= 512 && !(uneven && window == 0)) {
     per = blocks;
   } else if (per > most) {
     per = ceil_div(blocks * base, window > 0 ? 512 : 4096);
     if (per < most) per = most;
+    // Not more than a launch can count: a call is not refused for its splits.
+    if (base >= 512 && grid * ceil_div(blocks, per) >= (1 << 23)) per = blocks;
   }
   p.split_blocks = per < blocks ? (int)per : blocks;
   p.splits = ceil_div(blocks, p.split_blocks);
