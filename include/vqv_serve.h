@@ -188,7 +188,8 @@ typedef struct {
  *   y, out     [M, N] fp32, rows y_stride and out_stride elements apart (>= N):
  *              a projection's output or columns of a stacked one. 4-byte
  *              aligned (16-byte aligned rows are faster). out may be y itself
- *              with the same stride, else they may not overlap.
+ *              with the same stride, else they may not overlap (other columns
+ *              of the same rows do not).
  *   M          >= 0, M * N and M * K < 2^40, M < 2^22 (else
  *              VQV_ERR_UNSUPPORTED, as where a grid were too large: it is not
  *              while (M + 64) * min(n, 64) * (N + 1024) < 2^34).

@@ -249,3 +249,20 @@ def test_many_columns(vqv, case):
         c.a[e, r:] = float("nan")
         c.b[e, :, r:] = float("nan")
     c.close(vqv.vqv_lora_add(x, c.set(vqv), which, c.y.cuda()), c.want())
+
+
+@pytest.mark.parametrize("N", [99, 512, 8203])
+def test_other_columns_of_the_same_rows(vqv, N):
+    c = Case([0, -1, 1, 1, 0] * 13, K=64, N=N, rank=16, n=2)
+    ad, x, which = c.set(vqv), c.x.cuda(), c.which.cuda()
+    want = vqv.vqv_lora_add(x, ad, which, c.y.cuda())
+    for y0, o0 in ((0, N), (N + 3, 0)):
+        wide = torch.full((65, 2 * N + 5), 5.0, device="cuda")
+        y, out = wide[:, y0:y0 + N], wide[:, o0:o0 + N]
+        y.copy_(c.y)
+        vqv.vqv_lora_add(x, ad, which, y, out=out)
+        assert torch.equal(out, want) and torch.equal(y.cpu(), c.y)
+        rest = [i for i in range(2 * N + 5) if not (y0 <= i < y0 + N or o0 <= i < o0 + N)]
+        assert (wide[:, rest] == 5).all()
+    with pytest.raises(vqv.VqvError):
+        vqv.vqv_lora_add(x, ad, which, wide[:, :N], out=wide[:, 1:N + 1])

@@ -303,3 +303,12 @@ def test_long_sequences_are_split(S, L):
         s = seqs(S, n_seqs=n, n_rows=n, max_rows=1, max_kv=1 << 20, table_width=1 << 16, table_stride=1 << 16)
         c = cache(S, kv_heads=8, page_size=16)
         assert attn_call(S, L, c=c, s=s, heads=heads, ws=None, wn=0, q=None) == ARG   # refused for q, not for its size
+
+
+@pytest.mark.parametrize("off,width,ok", [(1000, 4000, True), (3000, 4000, True), (-1000, 4000, True),
+                                          (4000 * 3 + 2000, 4000, True), (999, 4000, False), (3001, 4000, False),
+                                          (4000 * 3, 4000, False), (1000, 1999, False), (-999, 4000, False)])
+def test_lora_columns_of_the_same_rows(S, L, off, width, ok):
+    """y and out as columns of one tensor do not overlap where the columns do not (off: elements)."""
+    status = lora_call(S, L, out=P[6] + 4 * off, ys=width, os=width)
+    assert (status != ARG) if ok else (status == ARG)

@@ -293,7 +293,7 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
   const int rest = part / a.seqs.n_seqs;
   // A sequence's tiles and splits go round the XCDs, pairs of them to the same (two tiles read the
   // same tokens). By numbers alone those of an even number of sequences go to a few only: a chunk of
-  // 256 rows beside 47 decoding rows 1390 us, so 437; 16 blocks of 16 rows to 16383 tokens 204 and 131.
+  // 256 rows beside 47 decoding rows 1390 us, so 404; 16 blocks of 16 rows to 16383 tokens 204 and 131.
   const int b = (part + (a.seqs.n_seqs % 2 ? 0 : rest / 2)) % a.seqs.n_seqs;
   const int group = a.groups - 1 - rest % a.groups;  // the longest first
   const int split = rest / a.groups;

@@ -241,6 +241,14 @@ vqv_status check_rows(const vqv_adapters& a, int M) {
   return vqv::lora_grids_fit(a, M) ? VQV_OK : VQV_ERR_UNSUPPORTED;
 }
 
+// Whether y and out are different columns of rows of one length.
+bool columns_apart(const float* y, const float* out, int N, int64_t y_stride, int64_t out_stride) {
+  if (y_stride != out_stride) return false;
+  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(out) - reinterpret_cast<uintptr_t>(y)) / 4 % y_stride;
+  if (d < 0) d += y_stride;
+  return d >= N && y_stride - d >= N;
+}
+
 }  // namespace
 
 extern "C" {
@@ -326,7 +334,9 @@ vqv_status vqv_lora_add(const void* x, vqv_dtype act_dtype, const vqv_adapters* 
   for (const Span& i : in)
     if (overlaps(out, ob, i.p, i.n) || overlaps(workspace, need, i.p, i.n)) return VQV_ERR_ARG;
   if (overlaps(workspace, need, y, yb) || overlaps(workspace, need, out, ob)) return VQV_ERR_ARG;
-  if (out == y ? out_stride != y_stride : overlaps(out, ob, y, yb)) return VQV_ERR_ARG;
+  if (out == y ? out_stride != y_stride
+               : overlaps(out, ob, y, yb) && !columns_apart(y, out, a.N, y_stride, out_stride))
+    return VQV_ERR_ARG;
   (void)hipGetLastError();
   return status_of(vqv::launch_lora_add(
       vqv::LoraArgs{x, a, which, M, y, y_stride, out, out_stride, workspace, nullptr, nullptr},
