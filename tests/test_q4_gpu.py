@@ -750,3 +750,15 @@ def test_chunk_beside_decoding_rows(vqv, n, dtype):
         c.close(c.run(vqv), c.want())
         c.max_kv = 9000     # planned for longer ones: splits
         c.close(c.run(vqv), c.want())
+
+
+def test_read_only_one(vqv):
+    cache, table, _ = append(vqv, rows=[4], kv=[10], heads=2, hk=1, dim=64, ps=16, rot=64, inter=False)
+    seqs = vqv.Sequences(i32([0, 4]), i32([10]), i32(table), n_rows=4, max_rows=4, max_kv=10)
+    k, v = vqv.vqv_cache_q4_read(cache, seqs)
+    for args in (dict(want_v=False), dict(k_out=torch.empty_like(k), want_k=False, want_v=False)):
+        got, none = vqv.vqv_cache_q4_read(cache, seqs, **args)
+        assert none is None and torch.equal(got, k)
+    none, got = vqv.vqv_cache_q4_read(cache, seqs, want_k=False)
+    assert none is None and torch.equal(got, v)
+    assert vqv.vqv_cache_q4_read(cache, seqs, want_k=False, want_v=False) == (None, None)

@@ -138,10 +138,11 @@ def vqv_rope_append_q4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cache:
 
 def vqv_cache_q4_read(cache: PagedCacheQ4, seqs: Sequences, layer: int = 0,
                       k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None,
-                      dtype: torch.dtype = torch.float32, stream=None):
+                      dtype: torch.dtype = torch.float32, stream=None, *, want_k: bool = True,
+                      want_v: bool = True):
     """(k, v) [n_rows, kv heads, dim]: the sequences' new rows as the cache
-    holds them, in the outputs' type or `dtype`. Rows that no sequence holds are
-    left as they were."""
+    holds them, in the outputs' type or `dtype`; None for one that is neither given
+    nor wanted. Rows that no sequence holds are left as they were."""
     dev = cache.device
     _same(dev, seqs=seqs)
     given = [t for t in (k_out, v_out) if t is not None]
@@ -150,10 +151,10 @@ def vqv_cache_q4_read(cache: PagedCacheQ4, seqs: Sequences, layer: int = 0,
         raise ValueError(f"unsupported type {dtype}")
     shape = (seqs.n_rows, cache.kv_heads, cache.dim)
 
-    def made(t):
-        return _new(shape, dtype, dev, stream) if t is None else t
+    def made(t, want):
+        return _new(shape, dtype, dev, stream) if t is None and want else t
 
-    k_out, v_out = made(k_out), made(v_out)
+    k_out, v_out = made(k_out, want_k), made(v_out, want_v)
     kp, vp = _take(k_out, "k_out", shape, dtype, dev), _take(v_out, "v_out", shape, dtype, dev)
     _check(_on_device(
         dev, _serve_lib().vqv_cache_q4_read, cache.c, layer, seqs.c, kp, vp, _DTYPES[dtype],
