@@ -555,9 +555,9 @@ AttnPlan attn_plan(const vqv_cache& c, const vqv_seqs& s, int heads, int window,
   return p;
 }
 
-size_t attn_partial_bytes(const vqv_cache& c, const vqv_seqs& s, int heads, const AttnPlan& p) {
+size_t attn_partial_bytes(int dim, const vqv_seqs& s, int heads, const AttnPlan& p) {
   if (p.splits <= 1) return 0;
-  return (size_t)s.n_rows * heads * p.splits * (c.dim + 2) * sizeof(float);
+  return (size_t)s.n_rows * heads * p.splits * (dim + 2) * sizeof(float);
 }
 
 namespace {

@@ -14,11 +14,7 @@ namespace {
 typedef __attribute__((ext_vector_type(4))) unsigned u32x4;
 typedef __attribute__((ext_vector_type(2))) unsigned u32x2;
 typedef __attribute__((ext_vector_type(4))) short s16x4;
-typedef __attribute__((ext_vector_type(8))) short s16x8;
-typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(16))) float f32x16;
-typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 constexpr unsigned kNoPlace = ~0u;
 constexpr float kLarge = 4096.0f;  // a shift below it is off by 2^-13 at most
@@ -213,16 +209,7 @@ __device__ __forceinline__ int page_index(const AttnArgs& a, int t) {
   return a.page_mul ? (int)(__umulhi((unsigned)t, a.page_mul) >> a.page_shift) : t;
 }
 
-// 16 (4) bytes per lane from global memory to LDS at `lds` (uniform) + 16 (4)
-// * lane, without registers between. These are no loads to the compiler, which
-// would wait for them before every LDS read: staged() waits for them. The
-// no-op covers the write of m0, which nothing else here uses.
-__device__ __forceinline__ void load16_to_lds(const void* from, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :
-               : "s"(lds), "v"(from)
-               : "memory");
-}
+// 4 bytes per lane, as load16_to_lds; staged() waits for both.
 __device__ __forceinline__ void load4_to_lds(const void* from, unsigned lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off"
                :
@@ -271,10 +258,6 @@ __device__ __forceinline__ float max_of_halves(float x) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
                                                   false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-
-__device__ __forceinline__ unsigned lds_offset(const void* p) {
-  return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
 }
 
 // LDS addresses of a lane's share of the keys and values of a staged block, for
@@ -468,8 +451,6 @@ __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a) {
         w;
   }
 }
-
-inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // What a call's arguments give the kernels, but for the cache's memory.
 inline AttnArgs attn_args(const void* q, void* out, const vqv_seqs& seqs, int page_size, int pages,

@@ -71,16 +71,6 @@ __device__ __forceinline__ int raw_piece(int row, int c) {
   return c;  // 3 and 5 have no common factor with 8
 }
 
-__device__ __forceinline__ f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
-
-template <typename V>
-__device__ __forceinline__ V lds_read(unsigned at) {
-  return *(__attribute__((address_space(3))) V*)at;
-}
-
 // The exponents of 1024 and 64 in both halves, for values of which each is the
 // offset. They are kept in vector registers: "and" and "or" are one instruction
 // only where one of two constants is.
@@ -252,10 +242,10 @@ __device__ __attribute__((noinline)) f32x4 product_with_bad_values(s16x8 v, Weig
     down[i] = out && (nan || (x & 0x8000u)) ? one : 0;
     see[i] = seen >> i & 1u ? one : 0;
   }
-  const f32x4 a = mfma16(up, see, f32x4{}), b = mfma16(down, see, f32x4{});
+  const f32x4 a = mfma16<_Float16>(up, see, f32x4{}), b = mfma16<_Float16>(down, see, f32x4{});
   const s16x8 f = finite<_Float16>(v);
-  o = mfma16(f, w.high, o);
-  if (FINE) o = mfma16(f, w.low, o);
+  o = mfma16<_Float16>(f, w.high, o);
+  if (FINE) o = mfma16<_Float16>(f, w.low, o);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (a[i] != 0.0f) o[i] += __builtin_inff();
@@ -270,7 +260,7 @@ __device__ __forceinline__ float max_of_quarters(float x) {
   return max_of_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
 }
 
-template <typename T, int D, int RT, int KW, int STAGES, bool FINE>
+template <typename T, int D, int RT, int KW, bool FINE>
 __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_attn_q4(
     const AttnArgs a) {
   typedef _Float16 H;
@@ -279,7 +269,8 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
   constexpr int R = q4_record_bytes(D), PC = R / 16;
   constexpr int ROWS = 16 * RT;
   constexpr int RAW = 64 * R;  // a stage: 32 records of keys, then of values
-  constexpr int RING = STAGES > 2 ? 8 : 4;  // blocks whose places are held
+  constexpr int STAGES = 2;    // blocks of records in LDS
+  constexpr int RING = 4;      // blocks whose places are held
   constexpr int OWN = STAGES * RAW + 2 * RING * 128;  // of a wave
   constexpr int PER = DT * 4 + 2;
   constexpr int JOIN = KW / 2 * PER * 256;
@@ -435,8 +426,8 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
         const Weights k = values_of_codes<HALF>(x.codes[e], x.meta[e], offsets);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          s[r][u] = mfma16(k.high, qf[r][e], e ? s[r][u] : f32x4{});
-          if (HALF) s[r][u] = mfma16(k.low, qf[r][e], s[r][u]);
+          s[r][u] = mfma16<_Float16>(k.high, qf[r][e], e ? s[r][u] : f32x4{});
+          if (HALF) s[r][u] = mfma16<_Float16>(k.low, qf[r][e], s[r][u]);
         }
       }
     }
@@ -558,8 +549,8 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
           if (bad) {
             to = product_with_bad_values<FINE>(v, w[r], seen[r], to);
           } else {
-            to = mfma16(v, w[r].high, to);
-            if (FINE) to = mfma16(v, w[r].low, to);
+            to = mfma16<_Float16>(v, w[r].high, to);
+            if (FINE) to = mfma16<_Float16>(v, w[r].low, to);
           }
         }
       }
@@ -588,10 +579,7 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
 
   for (int j = j0; j < j1; ++j) {
     // Block j is there; this wave's reads of block j - 1 are done.
-    if (STAGES > 2 && j + STAGES - 2 < j1)
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"((STAGES - 2) * PC) : "memory");
-    else
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     ask(j + 2 * STAGES - 1);
     if (j + STAGES - 1 < j1) load(j + STAGES - 1);
     if (j - j0 >= STAGES - 1) look_up(j + STAGES);
@@ -679,12 +667,11 @@ __global__ __launch_bounds__(KW * 64, D > 128 ? 1 : RT == 1 ? 3 : 2) void paged_
 
 // Waves of a work-group, each with blocks of its own.
 constexpr int waves(int dim) { return dim <= 128 ? 4 : 2; }
-constexpr int kStages = 2;
 
 template <typename T, int D, int RT, bool FINE>
 hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
   const int64_t grid = ((int64_t)a.seqs.n_seqs * a.groups * a.splits + 7) / 8 * 8 * a.kv_heads;
-  hipLaunchKernelGGL((paged_attn_q4<T, D, RT, waves(D), kStages, FINE>), dim3((unsigned)grid),
+  hipLaunchKernelGGL((paged_attn_q4<T, D, RT, waves(D), FINE>), dim3((unsigned)grid),
                      dim3(waves(D) * 64), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
@@ -732,12 +719,10 @@ int64_t pairs_of(const vqv_seqs& s, int heads, int kv_heads) {
 
 AttnPlan attn_q4_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int window, int sinks) {
   const int64_t m = pairs_of(s, heads, c.kv_heads);
-  AttnPlan p;
+  AttnPlan p{};
   p.mw = m <= 16 ? 1 : kMostTiles;
-  p.kw = waves(c.dim);
-  p.kt = 32;
   p.groups = ceil_div(m < 1 ? 1 : m, 16 * p.mw);
-  const int bt = p.kw * p.kt;
+  const int bt = waves(c.dim) * 32;
   // The most blocks that a tile's rows see.
   int64_t tokens = s.max_kv;
   if (window > 0) {
@@ -774,12 +759,6 @@ AttnPlan attn_q4_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int w
   p.split_blocks = per < blocks ? (int)per : blocks;
   p.splits = ceil_div(blocks, p.split_blocks);
   return p;
-}
-
-size_t attn_q4_partial_bytes(const vqv_cache_q4& c, const vqv_seqs& s, int heads,
-                             const AttnPlan& p) {
-  if (p.splits <= 1) return 0;
-  return (size_t)s.n_rows * heads * p.splits * (c.dim + 2) * sizeof(float);
 }
 
 hipError_t launch_paged_attn_q4(const void* q, int dtype, const vqv_cache_q4& c, int layer,

@@ -21,15 +21,11 @@
 // 18432, 19 us for 51 MB (2.6 TB/s); 8 rows of rank 16 10.5 us, which are two
 // launches and three waits for memory, one after the other, in each.
 
+#include "round_common.h"
 #include "serve_internal.h"
 
 namespace vqv {
 namespace {
-
-typedef __attribute__((ext_vector_type(8))) short s16x8;
-typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
-typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
-typedef __attribute__((ext_vector_type(4))) float f32x4;
 
 constexpr int kBlock = 64;       // rows that are looked at together
 constexpr int kShrinkWaves = 8;
@@ -39,19 +35,6 @@ template <typename T>
 constexpr bool kHalf = false;
 template <>
 constexpr bool kHalf<_Float16> = true;
-
-template <typename T>
-__device__ __forceinline__ f32x4 mfma16(s16x8 a, s16x8 b, f32x4 c);
-template <>
-__device__ __forceinline__ f32x4 mfma16<__bf16>(s16x8 a, s16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                 __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-template <>
-__device__ __forceinline__ f32x4 mfma16<_Float16>(s16x8 a, s16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-}
 
 // The adapter of a lane's row, -1 for none, and the slot-th distinct one of the
 // block with the rows that have it (adapter -1: there is none).
@@ -91,24 +74,8 @@ __device__ __forceinline__ int rank_of(const LoraArgs& a, int e) {
   return a.ad.ranks ? min(max(a.ad.ranks[e], 0), a.ad.rank) : a.ad.rank;
 }
 
-// 16 bytes per lane from global memory to LDS at `lds` (uniform) + 16 * lane;
-// the wait for them is loaded().
-__device__ __forceinline__ void load16_to_lds(const void* from, unsigned lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :
-               : "s"(lds), "v"(from)
-               : "memory");
-}
+// The wait for load16_to_lds.
 __device__ __forceinline__ void loaded() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
-
-template <typename V>
-__device__ __forceinline__ V lds_read(unsigned at) {
-  return *(__attribute__((address_space(3))) V*)(uintptr_t)at;
-}
-
-__device__ __forceinline__ unsigned lds_offset(const void* p) {
-  return (unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
-}
 
 // Which 16-byte piece of a staged row of `pieces` holds piece c, so that the
 // same piece of 8 rows lies in different banks (an exchange is its own inverse).
@@ -545,8 +512,6 @@ __global__ __launch_bounds__(kExpandWaves * 64) void lora_expand(const LoraArgs 
     }
   }
 }
-
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // How a call is cut.
 struct Plan {

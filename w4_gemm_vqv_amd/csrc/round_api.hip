@@ -196,7 +196,7 @@ size_t vqv_paged_attn_workspace_bytes(const vqv_cache* cache, const vqv_seqs* se
                                       int window, int sinks) {
   vqv::AttnPlan plan;
   if (plan_attn(cache, seqs, heads, window, sinks, &plan) != VQV_OK) return 0;
-  return vqv::attn_partial_bytes(*cache, *seqs, heads, plan);
+  return vqv::attn_partial_bytes(cache->dim, *seqs, heads, plan);
 }
 
 vqv_status vqv_paged_attn(const void* q, const vqv_cache* cache, int layer, const vqv_seqs* seqs,
@@ -209,7 +209,7 @@ vqv_status vqv_paged_attn(const void* q, const vqv_cache* cache, int layer, cons
   if (!(scale > 0.0f) || !isfinite(scale)) return VQV_ERR_ARG;
   if (!aligned(q, 16) || !aligned(out, 16)) return VQV_ERR_ALIGN;
   const size_t bytes = (size_t)seqs->n_rows * heads * cache->dim * 2;
-  const size_t need = vqv::attn_partial_bytes(*cache, *seqs, heads, plan);
+  const size_t need = vqv::attn_partial_bytes(cache->dim, *seqs, heads, plan);
   if (need && (!workspace || workspace_bytes < need || !aligned(workspace, 16)))
     return VQV_ERR_WORKSPACE;
   if (overlaps(out, bytes, q, bytes) || overlaps(workspace, need, q, bytes) ||

@@ -32,8 +32,7 @@ struct AttnPlan {
 };
 bool attn_dim_supported(int dim);
 AttnPlan attn_plan(const vqv_cache& cache, const vqv_seqs& seqs, int heads, int window, int sinks);
-size_t attn_partial_bytes(const vqv_cache& cache, const vqv_seqs& seqs, int heads,
-                          const AttnPlan& plan);
+size_t attn_partial_bytes(int dim, const vqv_seqs& seqs, int heads, const AttnPlan& plan);
 hipError_t launch_paged_attn(const void* q, const vqv_cache& cache, int layer,
                              const vqv_seqs& seqs, int heads, float scale, int window, int sinks,
                              void* out, void* workspace, const AttnPlan& plan,

@@ -139,10 +139,9 @@ vqv_status plan_attn_q4(const vqv_cache_q4* cache, const vqv_seqs* seqs, int hea
 // and the sums over it (at the workspace's start, in turn).
 size_t attn_q4_bytes(const vqv_cache_q4& cache, const vqv_seqs& seqs, int heads,
                      const vqv::AttnPlan& plan, const vqv::CopyPlan& copy) {
-  size_t part = vqv::attn_q4_partial_bytes(cache, seqs, heads, plan);
+  size_t part = vqv::attn_partial_bytes(cache.dim, seqs, heads, plan);
   if (copy.copied.slots == 0) return part;
-  const size_t wide =
-      vqv::attn_partial_bytes(vqv::copy_cache(cache, copy, nullptr), seqs, heads, copy.attn);
+  const size_t wide = vqv::attn_partial_bytes(cache.dim, seqs, heads, copy.attn);
   if (wide > part) part = wide;
   return (part + 15) / 16 * 16 + copy.bytes;
 }

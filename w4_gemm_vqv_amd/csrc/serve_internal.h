@@ -20,8 +20,6 @@ hipError_t launch_cache_q4_read(const vqv_cache_q4& cache, int layer, const vqv_
 
 AttnPlan attn_q4_plan(const vqv_cache_q4& cache, const vqv_seqs& seqs, int heads, int window,
                       int sinks);
-size_t attn_q4_partial_bytes(const vqv_cache_q4& cache, const vqv_seqs& seqs, int heads,
-                             const AttnPlan& plan);
 // The sequences that are not `copied`.
 hipError_t launch_paged_attn_q4(const void* q, int dtype, const vqv_cache_q4& cache, int layer,
                                 const vqv_seqs& seqs, int heads, float scale, int window,
