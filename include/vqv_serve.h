@@ -163,7 +163,8 @@ vqv_status vqv_verify_sampled(const float* logits, const int32_t* draft, const f
  * Adapters of a projection: a [n, rank, K] and b [n, N, rank], dense, 16-byte
  * aligned, bf16 or fp16; scale [n] fp32 on the device; ranks [n] int32 on the
  * device or NULL (all `rank`): of adapter e the first ranks[e] are used (cut to
- * 0..rank), the others are not read.
+ * 0..rank); the others have no influence, whatever they hold, but are read: a call
+ * costs what `rank` ranks cost.
  *   rank       a multiple of 8, 8..256; K a multiple of 8, 8 <= K <= 32768;
  *              1 <= N < 2^31 - 4096 (else VQV_ERR_ARG or, past the largest,
  *              VQV_ERR_UNSUPPORTED).
