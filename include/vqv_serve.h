@@ -90,7 +90,7 @@ vqv_status vqv_cache_q4_read(const vqv_cache_q4* cache, int layer, const vqv_seq
  * take fp16: values rounded once from scale * code + bias (2^-12 of a value; they
  * are to stay below 65504), keys so for bf16 queries and in two such numbers (to
  * 2^-22) for fp16 ones, bf16 queries times a power of two per row (a query value
- * 2^24 below its row's largest loses bits). The weights p_j, relative to the
+ * 2^27 below its row's largest loses bits). The weights p_j, relative to the
  * largest so far, are rounded once too; for fp16 outputs they are two numbers
  * (to 2^-22) where max_rows rows of a key head's queries are 64 or fewer.
  * Weights 2^29 below the largest are off by up to 2^-39 of it.

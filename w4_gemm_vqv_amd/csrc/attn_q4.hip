@@ -15,26 +15,30 @@
 // and the query rows are read in that order). Values: the transposing read of 4-bit
 // elements gives a lane one column's codes of 16 tokens, that of 16-bit elements
 // their scales and biases, so nothing but codes is moved. (Values made fp16 first,
-// written to LDS and read transposed: 229 us for decode instead of 164.)
+// written to LDS and read transposed: decode took 229 us for 164.)
 //
 // A code becomes fp16 by placing it under an exponent (1024 + q, or 64 + q for
 // those that stand 4 bits higher: no shift), subtracting that, which is exact,
 // and one fused multiply-add: 13 instructions for 8 values, and a single
 // rounding, 2^-12 of a value. bf16 queries become fp16 times a power of two per
-// row, exact but for values 2^24 below the row's largest. Keys of fp16 queries
+// row, exact but for values 2^27 below the row's largest. Keys of fp16 queries
 // stay in two fp16 values: rounded once, they would make the larger part of an
-// fp16 output's error.
+// fp16 output's error. Of bf16 calls keys, values and weights are one fp16 value
+// each; over 4096 tokens they add 2.2e-4, 1.9e-4 and 2.0e-4 (in all 3.5e-4) to the
+// 1.64e-3 that the output's own rounding is off by. Weights in two values would
+// leave 2.9e-4 of that, for 173 us of decoding instead of 165. Of fp16 calls values
+// are rounded once: 2.8e-4 in all, where a form in fp32 is off by 2.1e-4.
 //
-// All work-groups of a sequence's tokens run on one XCD whatever their key head:
-// with slots as the outer order the records of neighbouring heads share cache
-// lines (decode 229 us without that, 175 with).
+// All work-groups of a tile's or a split's tokens run on one XCD whatever their key
+// head: with slots as the outer order the records of neighbouring heads share cache
+// lines (decode took 229 us without that, 175 with).
 //
 // What bounds it, with 32 heads of 128 on 8 (a copy moves 4.8 TB/s here):
-//   48 ragged sequences to 16383 tokens, one row each: 164 us for 565 MB, 3.4 TB/s:
-//   the records' loads; the 16-bit cache takes 349 us for 1.8 GB.
+//   48 ragged sequences to 16383 tokens, one row each: 159 us for 565 MB, 3.6 TB/s:
+//   the records' loads; the 16-bit cache takes 355 us for 1.8 GB.
 //   8 rows over 4096 tokens: 15 us, two launches and a chain of waits, for 5 MB.
-//   16 sequences of 16 rows, 16 heads of 256 on 4 in fp16, a window of 4096: 125 us
-//   for 86 MB: forming keys in two values and weights in one for two tiles of rows.
+//   16 sequences of 16 rows, 16 heads of 256 on 4 in fp16, a window of 4096: 120 us
+//   for 86 MB: forming keys and weights in two values for two tiles of rows.
 // Large bf16 calls without a window go through copy_q4.hip instead.
 
 #include "attn_common.h"
@@ -683,7 +687,7 @@ hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
 
 // Tiles of 16 (row, head) pairs of a work-group, at most. With four the
 // registers of a wave hold no second block's work and spill (a prompt chunk of
-// 2048 rows over 10240 tokens: 1425 us, with two 730).
+// 2048 rows over 10240 tokens took 1425 us, with two it takes 730).
 constexpr int kMostTiles = 2;
 
 // Weights in two values: for fp16 outputs of up to 64 pairs. A bf16 output's own
@@ -738,7 +742,7 @@ AttnPlan attn_q4_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int w
   const int64_t base = c.kv_heads * tiles < grid ? c.kv_heads * tiles : grid;
   // Blocks of a split: as many as leave a work-group to each CU, and no more than
   // 1024 tokens' worth unless that were more than 16 rounds of work-groups (48
-  // ragged sequences: 164 us, with 2048 tokens 174, with 4096 201).
+  // ragged sequences: 161 us, with 2048 tokens 167, with 4096 194).
   // Where the rows alone fill the GPU: all, unless few work-groups have long
   // sequences, of which the longest would end alone (ragged to 16383 tokens, one
   // row each, split and whole: 64 sequences 217 and 277 us, 128 453 and 550; 32 x 16

@@ -5,7 +5,7 @@
 // tile of 32 (row, head) pairs. From kCopiedPairs pairs on it costs less to form
 // them once, into the workspace, and let the 16-bit cache's attention read them,
 // whose tiles have 256 pairs: 2048 rows over 10240 tokens, 32 heads of 128 on 8, take
-// 393 us, from the records 710 (heads of 256 1226 and 1982).
+// 393 to 414 us, from the records 730 (heads of 256 1245 and 1980).
 // The copy has pages of the cache's size, [page][head][slot][dim], and a table of
 // its own; a page that is not there is not there in the copy either. Sequences of
 // fewer rows, or longer than max_kv says, are read from the records.
@@ -28,9 +28,10 @@ constexpr int kTokens = 16;              // of a work-group
 constexpr size_t kMostBytes = 1u << 30;  // of a copy
 
 // Scores (rows * heads * tokens of the longest sequence) from which the copy pays
-// for itself and two more launches, with 32 heads of 128 on 8: at 2^27 114 us become
-// 88 (2048 rows of as many tokens) and 226 become 149 (128 of 32768); at 2^26 84
-// would become 128 (1024 of 2048), 96 100 (512 of 4096), but 124 92 (128 of 16384).
+// for itself and two more launches, with 32 heads of 128 on 8: at 2^27 117 us become
+// 85 (2048 rows of as many tokens), 177 140 (512 of 8192), 230 168 (128 of 32768) and
+// 165 163 (1024 of 4096); at 2^26 84 would become 123 (1024 of 2048), 97 97 (512 of
+// 4096), but 125 101 (128 of 16384).
 constexpr double kLeastScores = 1 << 27;
 
 struct CopyArgs {
@@ -49,8 +50,8 @@ struct CopyArgs {
 constexpr int threads(int dim) { return (kTokens * dim / 8 + 63) / 64 * 64; }  // whole waves
 
 // One thread per 8 values of a token's key and value head, a work-group per head:
-// 10240 tokens of 8 heads of 128 in 12.5 us, 55 MB at 4.4 TB/s (two heads to a
-// work-group 14.5, all eight 21).
+// 10240 tokens of 8 heads of 128 in 12 to 14 us, 55 MB at 4.2 TB/s (with two heads to
+// a work-group it took 14.5 where this took 12.5, with all eight 21).
 template <int D>
 __global__ __launch_bounds__(threads(D)) void copy_q4(const CopyArgs a) {
   constexpr int PER = D / 8;

@@ -16,10 +16,12 @@
 // neighbouring ranks (columns) of one row and moves them as 16 bytes.
 //
 // What bounds it, y not in a cache: 2100 rows of three adapters of rank 64, 5120 to
-// 17408 columns in fp16, take 115 us, 19 of them in the first kernel, for 320 MB
+// 17408 columns in fp16, take 113 us, 19 of them in the first kernel, for 320 MB
 // (2.8 TB/s; y and out are 292 MB of it); 64 rows of 40 adapters of rank 32, 2560 to
 // 18432, 19 us for 51 MB (2.6 TB/s); 8 rows of rank 16 10.5 us, which are two
-// launches and three waits for memory, one after the other, in each.
+// launches and three waits for memory, one after the other, in each. Ranks of 72 to
+// 128 take 83 KB of LDS, one work-group to a CU, and those past 128 16 columns at a time:
+// 64 rows of 40 adapters of rank 64, 96, 128, 136 and 256 take 31, 80, 77, 235 and 295 us.
 
 #include "round_common.h"
 #include "serve_internal.h"
@@ -533,8 +535,8 @@ Plan plan_of(const vqv_adapters& ad, int M) {
   if (splits > steps / 16) splits = steps / 16;
   if (splits > 8) splits = 8;
   p.splits = splits < 1 ? 1 : splits;
-  // Columns of a work-group of the second kernel: 128 to a wave, 64 at a time (2100
-  // rows, rank 64: 115 us, with 64 120, with 256 132; 64 rows of 40 adapters of rank
+  // Columns of a work-group of the second kernel: 128 to a wave, 64 at a time (in one
+  // session 2100 rows of rank 64: 115 us, with 64 120, with 256 132; 64 rows of 40 adapters of rank
   // 32: 19.3, 21.5, 23.7), or 16 where 64 leave fewer than one work-group to a CU if
   // an eighth of the slots are taken, or the weights of 64 would take all of a CU's LDS.
   const int64_t some = (int64_t)p.blocks * (p.slots / 8 > 1 ? p.slots / 8 : 1);

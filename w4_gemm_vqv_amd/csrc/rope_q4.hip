@@ -9,9 +9,10 @@
 // neighbouring threads hold a group of 32, exchange its least and largest value,
 // and write its 16 bytes of codes, the first of them its scale and bias.
 //
-// What bounds it, with 32 query heads and 8 key heads of 128: 8 rows take 8.7 us, the
+// What bounds it, with 32 query heads and 8 key heads of 128: 8 rows take 9 us, the
 // chain of row, length, page, sine and rotation; 4 ragged chunks of up to 2048 rows
-// 30 us, with the read of the new rows in fp32 (11.6 us) 141 MB at 3.4 TB/s.
+// 30 to 34 us, as a row's own values are asked for behind that chain; with the read of
+// the new rows in fp32 (12 us) 45 us for 141 MB, 3.1 TB/s.
 
 #include "round_common.h"
 #include "serve_internal.h"

@@ -17,9 +17,10 @@
 //
 // What bounds it: the 64-bit exponentials beside the loads in the first kernel (64
 // rows of 151936 logits: 13 us, 3 TB/s); the second is a chain of passes over a
-// row's chunks, with a wait for the last work-group between, of 7 to 10.5 us.
-// Together, for 1 x 8 and 4 x 16 rows with draft probabilities and 64 x 1: 15, 19
-// and 19 us. With sums by LDS atomics and 256 threads a draw: 31, 37 and 35.
+// row's chunks, with a wait for the last work-group between, of 7 to 10 us.
+// A call of 1 x 8 and 4 x 16 rows with draft probabilities and of 64 x 1: 14, 16 to 19
+// (as blocks end) and 19 us. With sums by LDS atomics and 256 threads a draw they
+// took 31, 37 and 35.
 
 #include <limits.h>
 
