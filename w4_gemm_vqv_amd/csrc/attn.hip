@@ -54,6 +54,7 @@ template <typename T, int D, int MW, int KW, int KT, int STAGES, typename TO>
 __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void paged_attn(
     const AttnArgs a) {
   constexpr int NW = MW * KW, BT = KW * KT, DC = D / 8, DS = D / 16, DB = (D + 31) / 32;
+  constexpr bool SAME = Bits<T>::exponent == Bits<TO>::exponent;  // else only the sequences of a copy
   constexpr bool PAIRS = MW == 8;
   constexpr bool FINE = MW <= 2;
   constexpr int ROWS = PAIRS ? 128 : 32 * MW;        // (row, head) pairs of a tile
@@ -92,7 +93,9 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
   const Tiles tile = tiles_of<PAIRS>(group, tiles);
   const int pos0 = max(a.seqs.kv_len[b], 0) - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
   const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
-  if (not_of_this_call(a, b)) return;
+  if constexpr (!SAME) {
+    if (not_of_this_call(a, b)) return;
+  }
   const Blocks blocks =
       visible_blocks<BT>(pos0 + tile.first * ROWS / g,
                          pos0 + (min((tile.second + 1) * ROWS, pairs) - 1) / g, kv_len, a.window,
@@ -126,7 +129,6 @@ __global__ __launch_bounds__(MW * KW * 64, MW >= 4 && D <= 128 ? 2 : 1) void pag
 
   // bf16 queries of fp16 products: times a power of two for each row, which the
   // scale of its scores takes back.
-  constexpr bool SAME = Bits<T>::exponent == Bits<TO>::exponent;
   int shift_q = 0;
   if constexpr (!SAME) {
     unsigned top = 0;
@@ -450,7 +452,8 @@ hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
                      dim3(MW * KW * 64), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((paged_attn_join<TO, D, KW * KT, MW == 8 ? 128 : 32 * MW, MW == 8>),
+  hipLaunchKernelGGL((paged_attn_join<TO, D, KW * KT, MW == 8 ? 128 : 32 * MW, MW == 8,
+                                      Bits<T>::exponent != Bits<TO>::exponent>),
                      dim3((unsigned)(a.seqs.n_rows * a.kv_heads * a.group)), dim3(256), 0, stream,
                      a);
   return hipGetLastError();

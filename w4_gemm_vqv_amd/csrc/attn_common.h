@@ -394,8 +394,9 @@ __device__ __forceinline__ int group_of(int tile, int tiles) {
 }
 
 // Joins the partial sums of a (row, head): one work-group, 4 columns per
-// thread, so that 1024 / D (rounded down) parts are read at the same time.
-template <typename T, int D, int BT, int ROWS, bool PAIRS>
+// thread, so that 1024 / D (rounded down) parts are read at the same time. SOME: the
+// launch may be for some of the sequences.
+template <typename T, int D, int BT, int ROWS, bool PAIRS, bool SOME>
 __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a) {
   constexpr int COLS = D / 4, SETS = 256 / COLS;
   __shared__ f32x4 sums[SETS][COLS];
@@ -410,7 +411,7 @@ __global__ __launch_bounds__(256) void paged_attn_join(const AttnArgs a) {
   const int g = a.group, tiles = (n * g + ROWS - 1) / ROWS;
   const int pos0 = max(a.seqs.kv_len[b], 0) - (a.seqs.row_start[b + 1] - a.seqs.row_start[b]);
   const int kv_len = tokens_of(a, a.seqs.kv_len[b]);
-  if (not_of_this_call(a, b)) return;
+  if (SOME && not_of_this_call(a, b)) return;
   const Tiles tile =
       tiles_of<PAIRS>(group_of<PAIRS>(((r - row0) * g + head % g) / ROWS, tiles), tiles);
   const Blocks blocks =

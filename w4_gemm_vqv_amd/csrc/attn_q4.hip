@@ -35,7 +35,7 @@
 //
 // What bounds it, with 32 heads of 128 on 8 (a copy moves 4.8 TB/s here):
 //   48 ragged sequences to 16383 tokens, one row each: 159 us for 565 MB, 3.6 TB/s:
-//   the records' loads; the 16-bit cache takes 355 us for 1.8 GB.
+//   the records' loads; the 16-bit cache takes 351 us for 1.8 GB.
 //   8 rows over 4096 tokens: 15 us, two launches and a chain of waits, for 5 MB.
 //   16 sequences of 16 rows, 16 heads of 256 on 4 in fp16, a window of 4096: 120 us
 //   for 86 MB: forming keys and weights in two values for two tiles of rows.
@@ -679,7 +679,7 @@ hipError_t launch_shape(const AttnArgs& a, hipStream_t stream) {
                      dim3(waves(D) * 64), 0, stream, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || a.splits == 1) return e;
-  hipLaunchKernelGGL((paged_attn_join<T, D, waves(D) * 32, 16 * RT, false>),
+  hipLaunchKernelGGL((paged_attn_join<T, D, waves(D) * 32, 16 * RT, false, true>),
                      dim3((unsigned)(a.seqs.n_rows * a.kv_heads * a.group)), dim3(256), 0, stream,
                      a);
   return hipGetLastError();

@@ -536,7 +536,7 @@ Plan plan_of(const vqv_adapters& ad, int M) {
   if (splits > 8) splits = 8;
   p.splits = splits < 1 ? 1 : splits;
   // Columns of a work-group of the second kernel: 128 to a wave, 64 at a time (in one
-  // session 2100 rows of rank 64: 115 us, with 64 120, with 256 132; 64 rows of 40 adapters of rank
+  // run 2100 rows of rank 64: 115 us, with 64 120, with 256 132; 64 rows of 40 adapters of rank
   // 32: 19.3, 21.5, 23.7), or 16 where 64 leave fewer than one work-group to a CU if
   // an eighth of the slots are taken, or the weights of 64 would take all of a CU's LDS.
   const int64_t some = (int64_t)p.blocks * (p.slots / 8 > 1 ? p.slots / 8 : 1);
