@@ -312,3 +312,9 @@ def test_lora_columns_of_the_same_rows(S, L, off, width, ok):
     """y and out as columns of one tensor do not overlap where the columns do not (off: elements)."""
     status = lora_call(S, L, out=P[6] + 4 * off, ys=width, os=width)
     assert (status != ARG) if ok else (status == ARG)
+
+
+def test_not_refused_for_splits(S, L):
+    """Rows past max_rows are not computed, but they count where partial sums are joined."""
+    s = seqs(S, n_seqs=64, n_rows=1 << 20, max_rows=1, max_kv=1 << 15, table_width=1 << 11, table_stride=1 << 11)
+    assert attn_call(S, L, s=s, ws=None, wn=0, q=None) == ARG   # refused for q, not for its size

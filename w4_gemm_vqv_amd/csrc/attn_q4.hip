@@ -758,7 +758,9 @@ AttnPlan attn_q4_plan(const vqv_cache_q4& c, const vqv_seqs& s, int heads, int w
     per = ceil_div(blocks * base, window > 0 ? 512 : 4096);
     if (per < most) per = most;
     // Not more than a launch can count: a call is not refused for its splits.
-    if (base >= 512 && grid * ceil_div(blocks, per) >= (1 << 23)) per = blocks;
+    if (base >= 512 && (grid * ceil_div(blocks, per) >= (1 << 23) ||
+                        (int64_t)s.n_rows * heads >= (1 << 24)))
+      per = blocks;
   }
   p.split_blocks = per < blocks ? (int)per : blocks;
   p.splits = ceil_div(blocks, p.split_blocks);
